@@ -100,6 +100,20 @@ gnf4_status check_ptr(const void* p, const char* name, size_t align, bool requir
   return GNF4_OK;
 }
 
+// check_ptr, and the memory belongs to the device the kernel will run on (managed memory belongs to all).
+gnf4_status check_local_ptr(const void* p, const char* name, size_t align, bool required = true) {
+  gnf4_status st = check_ptr(p, name, align, required);
+  if (st != GNF4_OK || p == nullptr) return st;
+  int dev = -1;
+  cudaPointerAttributes a;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaPointerGetAttributes(&a, p);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes");
+  if (a.type == cudaMemoryTypeDevice && a.device != dev)
+    return fail(GNF4_ERR_INVALID_ARG, "%s is memory of device %d, the current device is %d", name, a.device, dev);
+  return GNF4_OK;
+}
+
 #define GNF4_TRY(x)                  \
   do {                               \
     gnf4_status _s = (x);            \
@@ -1043,6 +1057,240 @@ gnf4_status gnf4_grouped_gemv_mxfp4_swiglu(const void* a, const uint8_t* w_gate_
   CallScope call(Entry::grouped_gemv_mxfp4_swiglu, (long long)M);
   return call(grouped_swiglu(true, 1, a, w_gate_up, scales, offsets, counts, E, I, K, M, h,
                              stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- whole layer for a few tokens
+
+static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w, const float* bias, float* logits,
+                                   int T, int E, int k, int H, int I, const uint8_t* w_gate_up,
+                                   const void* scales_gate_up, const uint8_t* w_down, const void* scales_down,
+                                   int32_t* topk_ids, float* topk_weights, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (T < 0 || T > kMoeDecodeMaxTokens)
+    return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "T=%d outside [0, %d]", T, kMoeDecodeMaxTokens);
+  if (E < 1 || E > kMaxExperts) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "E=%d outside [1, %d]", E, kMaxExperts);
+  if (k < 1 || k > E || k > kMaxRouterTopK)
+    return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "k=%d outside [1, min(E=%d, %d)]", k, E, kMaxRouterTopK);
+  const int kq = fmt == 0 ? 64 : 32;
+  if (H < kq || H % kq != 0 || H > kMoeDecodeMaxTH)
+    return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "H=%d (K=H) must be a multiple of %d in [%d, %d]", H, kq, kq, kMoeDecodeMaxTH);
+  if (I < kq || I % kq != 0 || I > 65536)
+    return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I=%d must be a multiple of %d in [%d, 65536]", I, kq, kq);
+  if (T * H > kMoeDecodeMaxTH)
+    return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "T=%d times H=%d exceeds %d", T, H, kMoeDecodeMaxTH);
+  if (T == 0) return GNF4_OK;
+  const char* sname = fmt == 0 ? "absmax_gate_up" : "scales_gate_up";
+  const char* sname2 = fmt == 0 ? "absmax_down" : "scales_down";
+  GNF4_TRY(check_local_ptr(x, "x", 16));
+  GNF4_TRY(check_local_ptr(router_w, "router_w", 16, false));
+  GNF4_TRY(check_local_ptr(bias, "bias", 4, false));
+  GNF4_TRY(check_local_ptr(logits, "logits", 4));
+  GNF4_TRY(check_local_ptr(w_gate_up, "w_gate_up", 16));
+  GNF4_TRY(check_local_ptr(scales_gate_up, sname, fmt == 0 ? 4 : 1));
+  GNF4_TRY(check_local_ptr(w_down, "w_down", 16));
+  GNF4_TRY(check_local_ptr(scales_down, sname2, fmt == 0 ? 4 : 1));
+  GNF4_TRY(check_local_ptr(topk_ids, "topk_ids", 4));
+  GNF4_TRY(check_local_ptr(topk_weights, "topk_weights", 4));
+  GNF4_TRY(check_local_ptr(out, "out", 16));
+  size_t count_at, part_at, h_at;
+  const size_t need = moe_decode_workspace(T, k, H, I, &count_at, &part_at, &h_at);
+  if (workspace_bytes < need)
+    return fail(GNF4_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
+                need);
+  GNF4_TRY(check_local_ptr(workspace, "workspace", 16));
+  DeviceState* d = nullptr;
+  GNF4_TRY(device_state(&d));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MoeDecodeArgs p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.router_w = static_cast<const __nv_bfloat16*>(router_w);
+  p.bias = bias;
+  p.logits = logits;
+  p.w1 = w_gate_up, p.s1 = scales_gate_up;
+  p.w2 = w_down, p.s2 = scales_down;
+  p.topk_ids = topk_ids, p.topk_weights = topk_weights;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.sync = reinterpret_cast<unsigned*>(ws);
+  p.unit_count = reinterpret_cast<unsigned*>(ws + count_at);
+  p.part = reinterpret_cast<float*>(ws + part_at);
+  p.hbuf = reinterpret_cast<__nv_bfloat16*>(ws + h_at);
+  p.err = d->err;
+  p.T = T, p.E = E, p.k = k, p.H = H, p.I = I;
+  cudaError_t e = launch_moe_decode(fmt, p, d->num_sms, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "MoE decode launch");
+  note_launch(kPathOther);
+  return GNF4_OK;
+}
+
+extern "C" {
+
+size_t gnf4_moe_decode_workspace_bytes(int T, int k, int H, int I) {
+  if (T < 1 || T > kMoeDecodeMaxTokens || k < 1 || k > kMaxRouterTopK || H < 32 || I < 32 || I > 65536 ||
+      H > kMoeDecodeMaxTH)
+    return 0;
+  size_t a, b, c;
+  return moe_decode_workspace(T, k, H, I, &a, &b, &c);
+}
+
+gnf4_status gnf4_moe_decode_nf4(const void* x, const void* router_w, const float* bias, float* logits, int T, int E,
+                                int k, int H, int I, const uint8_t* w_gate_up, const float* absmax_gate_up,
+                                const uint8_t* w_down, const float* absmax_down, int32_t* topk_ids,
+                                float* topk_weights, void* out, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  CallScope call(Entry::moe_decode_nf4, (long long)T * k);
+  return call(moe_decode_impl(0, x, router_w, bias, logits, T, E, k, H, I, w_gate_up, absmax_gate_up, w_down,
+                              absmax_down, topk_ids, topk_weights, out, workspace, workspace_bytes, stream));
+}
+
+gnf4_status gnf4_moe_decode_mxfp4(const void* x, const void* router_w, const float* bias, float* logits, int T, int E,
+                                  int k, int H, int I, const uint8_t* w_gate_up, const uint8_t* scales_gate_up,
+                                  const uint8_t* w_down, const uint8_t* scales_down, int32_t* topk_ids,
+                                  float* topk_weights, void* out, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  CallScope call(Entry::moe_decode_mxfp4, (long long)T * k);
+  return call(moe_decode_impl(1, x, router_w, bias, logits, T, E, k, H, I, w_gate_up, scales_gate_up, w_down,
+                              scales_down, topk_ids, topk_weights, out, workspace, workspace_bytes, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- training: 8-bit SwiGLU checkpoint, backward passes
+
+static gnf4_status check_ckpt8_shape(int M, int I) {
+  if (M < 0) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "M=%d is negative", M);
+  if (I < 32 || I % 32 != 0) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I=%d must be a positive multiple of 32", I);
+  if ((long long)M * I > (1LL << 40)) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "M=%d times I=%d is too large", M, I);
+  return GNF4_OK;
+}
+
+static gnf4_status swiglu_ckpt8_impl(const void* gate_up, int M, int I, const int32_t* num_rows, void* h,
+                                     uint8_t* codes, uint8_t* scales, void* stream) {
+  GNF4_TRY(check_ckpt8_shape(M, I));
+  if (M == 0) return GNF4_OK;
+  GNF4_TRY(check_local_ptr(gate_up, "gate_up", 16));
+  GNF4_TRY(check_local_ptr(num_rows, "num_rows", 4, false));
+  GNF4_TRY(check_local_ptr(h, "h", 16));
+  GNF4_TRY(check_local_ptr(codes, "codes", 16));
+  GNF4_TRY(check_local_ptr(scales, "scales", 1));
+  DeviceState* d = nullptr;
+  GNF4_TRY(device_state(&d));
+  cudaError_t e = launch_swiglu_ckpt8(static_cast<const __nv_bfloat16*>(gate_up), M, I, num_rows,
+                                      static_cast<__nv_bfloat16*>(h), codes, scales, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "SwiGLU checkpoint launch");
+  note_launch(kPathOther);
+  return GNF4_OK;
+}
+
+static gnf4_status swiglu_ckpt8_backward_impl(const void* dh, const uint8_t* codes, const uint8_t* scales,
+                                              const int32_t* num_rows, const int32_t* sorted_to_flat,
+                                              const int32_t* flat_to_sorted, const float* weights, int M, int I,
+                                              void* d_gate_up, void* h, float* d_weights, void* stream) {
+  GNF4_TRY(check_ckpt8_shape(M, I));
+  if (weights != nullptr && sorted_to_flat == nullptr)
+    return fail(GNF4_ERR_INVALID_ARG, "weights need sorted_to_flat");
+  if (d_weights != nullptr && (sorted_to_flat == nullptr || flat_to_sorted == nullptr))
+    return fail(GNF4_ERR_INVALID_ARG, "d_weights need sorted_to_flat and flat_to_sorted");
+  if (M == 0) return GNF4_OK;
+  GNF4_TRY(check_local_ptr(dh, "dh", 16));
+  GNF4_TRY(check_local_ptr(codes, "codes", 16));
+  GNF4_TRY(check_local_ptr(scales, "scales", 1));
+  GNF4_TRY(check_local_ptr(num_rows, "num_rows", 4, false));
+  GNF4_TRY(check_local_ptr(sorted_to_flat, "sorted_to_flat", 4, false));
+  GNF4_TRY(check_local_ptr(flat_to_sorted, "flat_to_sorted", 4, false));
+  GNF4_TRY(check_local_ptr(weights, "weights", 4, false));
+  GNF4_TRY(check_local_ptr(d_gate_up, "d_gate_up", 16));
+  GNF4_TRY(check_local_ptr(h, "h", 16, false));
+  GNF4_TRY(check_local_ptr(d_weights, "d_weights", 4, false));
+  DeviceState* d = nullptr;
+  GNF4_TRY(device_state(&d));
+  cudaError_t e = launch_swiglu_ckpt8_backward(static_cast<const __nv_bfloat16*>(dh), codes, scales, num_rows,
+                                               sorted_to_flat, flat_to_sorted, weights, M, I,
+                                               static_cast<__nv_bfloat16*>(d_gate_up), static_cast<__nv_bfloat16*>(h),
+                                               d_weights, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "SwiGLU checkpoint backward launch");
+  note_launch(kPathOther);
+  return GNF4_OK;
+}
+
+static gnf4_status combine_backward_impl(const void* dout, const void* y, const int32_t* sorted_to_flat,
+                                         const int32_t* flat_to_sorted, const float* weights, int T, int k, int N,
+                                         void* dy, float* d_weights, void* stream) {
+  if (T < 0) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "T=%d is negative", T);
+  if (k < 1) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "k=%d must be positive", k);
+  if ((long long)T * k >= (1LL << 31)) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "T*k too large");
+  if (N < 8 || N % 8 != 0) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "N=%d must be a positive multiple of 8", N);
+  if (d_weights != nullptr && (y == nullptr || flat_to_sorted == nullptr))
+    return fail(GNF4_ERR_INVALID_ARG, "d_weights need y and flat_to_sorted");
+  if (T == 0) return GNF4_OK;
+  GNF4_TRY(check_local_ptr(dout, "dout", 16));
+  GNF4_TRY(check_local_ptr(y, "y", 16, false));
+  GNF4_TRY(check_local_ptr(sorted_to_flat, "sorted_to_flat", 4));
+  GNF4_TRY(check_local_ptr(flat_to_sorted, "flat_to_sorted", 4, false));
+  GNF4_TRY(check_local_ptr(weights, "weights", 4, false));
+  GNF4_TRY(check_local_ptr(dy, "dy", 16));
+  GNF4_TRY(check_local_ptr(d_weights, "d_weights", 4, false));
+  DeviceState* d = nullptr;
+  GNF4_TRY(device_state(&d));
+  // without d_weights y is not read
+  cudaError_t e = launch_combine_backward(static_cast<const __nv_bfloat16*>(dout),
+                                          d_weights != nullptr ? static_cast<const __nv_bfloat16*>(y) : nullptr,
+                                          sorted_to_flat, flat_to_sorted, weights, T * k, k, N,
+                                          static_cast<__nv_bfloat16*>(dy), d_weights, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "combine backward launch");
+  note_launch(kPathOther);
+  return GNF4_OK;
+}
+
+static gnf4_status route_topk_backward_impl(const int32_t* topk_ids, const float* topk_weights,
+                                            const float* d_weights, int T, int k, int E, float* d_logits,
+                                            void* stream) {
+  if (T < 0) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "T=%d is negative", T);
+  if (E < 1 || E > 4096) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "E=%d outside [1, 4096]", E);
+  if (k < 1 || k > E || k > kMaxRouterTopK)
+    return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "k=%d outside [1, min(E=%d, %d)]", k, E, kMaxRouterTopK);
+  if (T == 0) return GNF4_OK;
+  GNF4_TRY(check_local_ptr(topk_ids, "topk_ids", 4));
+  GNF4_TRY(check_local_ptr(topk_weights, "topk_weights", 4));
+  GNF4_TRY(check_local_ptr(d_weights, "d_weights", 4));
+  GNF4_TRY(check_local_ptr(d_logits, "d_logits", 4));
+  DeviceState* d = nullptr;
+  GNF4_TRY(device_state(&d));
+  cudaError_t e = launch_route_topk_backward(topk_ids, topk_weights, d_weights, T, k, E, d_logits, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "router backward launch");
+  note_launch(kPathOther);
+  return GNF4_OK;
+}
+
+extern "C" {
+
+gnf4_status gnf4_swiglu_ckpt8(const void* gate_up, int M, int I, const int32_t* num_rows, void* h, uint8_t* codes,
+                              uint8_t* scales, void* stream) {
+  CallScope call(Entry::swiglu_ckpt8, (long long)M);
+  return call(swiglu_ckpt8_impl(gate_up, M, I, num_rows, h, codes, scales, stream));
+}
+
+gnf4_status gnf4_swiglu_ckpt8_backward(const void* dh, const uint8_t* codes, const uint8_t* scales,
+                                       const int32_t* num_rows, const int32_t* sorted_to_flat,
+                                       const int32_t* flat_to_sorted, const float* weights, int M, int I,
+                                       void* d_gate_up, void* h, float* d_weights, void* stream) {
+  CallScope call(Entry::swiglu_ckpt8_backward, (long long)M);
+  return call(swiglu_ckpt8_backward_impl(dh, codes, scales, num_rows, sorted_to_flat, flat_to_sorted, weights, M, I,
+                                         d_gate_up, h, d_weights, stream));
+}
+
+gnf4_status gnf4_combine_backward(const void* dout, const void* y, const int32_t* sorted_to_flat,
+                                  const int32_t* flat_to_sorted, const float* weights, int T, int k, int N, void* dy,
+                                  float* d_weights, void* stream) {
+  CallScope call(Entry::combine_backward, (long long)T * k);
+  return call(combine_backward_impl(dout, y, sorted_to_flat, flat_to_sorted, weights, T, k, N, dy, d_weights, stream));
+}
+
+gnf4_status gnf4_route_topk_backward(const int32_t* topk_ids, const float* topk_weights, const float* d_weights,
+                                     int T, int k, int E, float* d_logits, void* stream) {
+  CallScope call(Entry::route_topk_backward, (long long)T * k);
+  return call(route_topk_backward_impl(topk_ids, topk_weights, d_weights, T, k, E, d_logits, stream));
 }
 
 }  // extern "C"

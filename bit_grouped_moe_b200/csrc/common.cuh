@@ -9,6 +9,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -141,6 +142,24 @@ __device__ __forceinline__ float silu_mul_tanh(float g, float u) {
   asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(hg));
   return fmaf(hg, t, hg) * u;
 }
+
+// ---------------------------------------------------------------- e4m3
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
+  uint16_t pr;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pr) : "f"(hi), "f"(lo));
+  return pr;
+}
+
+// e4m3 pair (low byte = first element) -> two floats, exactly (through f16).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t pr) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pr));
+  const __half2 hh = *reinterpret_cast<const __half2*>(&h);
+  return __half22float2(hh);
+}
+
+// Exact power of two 2^e for e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // ---------------------------------------------------------------- stream order
 // Programmatic dependent launch: let the next kernel of the stream be

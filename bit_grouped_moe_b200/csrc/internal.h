@@ -156,6 +156,46 @@ constexpr int kMaxRouterTopK = 32;
 cudaError_t launch_combine(const __nv_bfloat16* y, const int32_t* flat_to_sorted, const float* weights, int T,
                            int k, int N, __nv_bfloat16* out, int num_sms, cudaStream_t stream);
 
+// ckpt8.cu: SwiGLU with gate_up kept as MXFP8 (one binade of headroom), and its backward pass
+cudaError_t launch_swiglu_ckpt8(const __nv_bfloat16* gate_up, int M, int I, const int32_t* num_rows,
+                                __nv_bfloat16* h, uint8_t* codes, uint8_t* scales, cudaStream_t stream);
+cudaError_t launch_swiglu_ckpt8_backward(const __nv_bfloat16* dh, const uint8_t* codes, const uint8_t* scales,
+                                         const int32_t* num_rows, const int32_t* s2f, const int32_t* f2s,
+                                         const float* weights, int M, int I, __nv_bfloat16* d_gate_up,
+                                         __nv_bfloat16* h, float* d_weights, cudaStream_t stream);
+
+// backward.cu: backward of the combine (y null: d_weights null) and of the router epilogue
+cudaError_t launch_combine_backward(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* s2f,
+                                    const int32_t* f2s, const float* weights, int M, int k, int N,
+                                    __nv_bfloat16* dy, float* d_weights, cudaStream_t stream);
+cudaError_t launch_route_topk_backward(const int32_t* ids, const float* probs, const float* d_weights, int T, int k,
+                                       int E, float* d_logits, cudaStream_t stream);
+
+// moe_decode.cu: a whole routed layer for a few tokens (cooperative launch over every SM)
+constexpr int kMoeDecodeMaxTokens = 8;
+constexpr int kMoeDecodeMaxTH = 57344;  // T * H: x lies in shared memory
+struct MoeDecodeArgs {
+  const __nv_bfloat16* x;         // [T, H]
+  const __nv_bfloat16* router_w;  // [E, H] or null: logits are given
+  const float* bias;              // [E] or null
+  float* logits;                  // [T, E]
+  const uint8_t* w1;              // [E, 2I, H/2]
+  const void* s1;
+  const uint8_t* w2;              // [E, H, I/2]
+  const void* s2;
+  int* topk_ids;                  // [T, k]
+  float* topk_weights;            // [T, k]
+  __nv_bfloat16* out;             // [T, H]
+  unsigned* sync;                 // workspace: barrier words, zero between calls
+  unsigned* unit_count;           // workspace: [H/16], zero between calls
+  float* part;                    // workspace: partial sums of output tiles split between CTAs
+  __nv_bfloat16* hbuf;            // workspace: [T*k, I padded to 128], in MMA fragment order
+  unsigned* err;
+  int T, E, k, H, I;
+};
+size_t moe_decode_workspace(int T, int k, int H, int I, size_t* count_at, size_t* part_at, size_t* h_at);
+cudaError_t launch_moe_decode(int fmt, const MoeDecodeArgs& p, int num_sms, cudaStream_t stream);
+
 // selftest.cu: one bounded wait on a barrier nothing arrives on
 cudaError_t launch_bounded_wait_probe(unsigned* err, long long limit_cycles, cudaStream_t stream);
 
@@ -170,7 +210,9 @@ void set_last_error(const char* msg);
   X(grouped_gemv_nf4_swiglu) X(grouped_gemv_mxfp4_swiglu) X(grouped_gemv_nf4_combine)                     \
   X(grouped_gemv_mxfp4_combine) X(grouped_gemm_nf4_combine) X(grouped_gemm_mxfp4_combine)                 \
   X(quantize_mxfp8) X(quantize_mxfp8_split) X(quantize_mxfp4_act) X(grouped_gemm_w4a8)                    \
-  X(grouped_gemm_w4a8x2) X(grouped_gemm_w4a4) X(combine) X(dequant_nf4_f32) X(dequant_mxfp4_f32)
+  X(grouped_gemm_w4a8x2) X(grouped_gemm_w4a4) X(combine) X(dequant_nf4_f32) X(dequant_mxfp4_f32)                 \
+  X(moe_decode_nf4) X(moe_decode_mxfp4) X(swiglu_ckpt8) X(swiglu_ckpt8_backward)                          \
+  X(combine_backward) X(route_topk_backward)
 
 enum class Entry : int {
 #define GNF4_ENTRY_ENUM(n) n,

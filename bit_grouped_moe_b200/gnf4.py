@@ -71,7 +71,17 @@ _lib.gnf4_call_stats_get.argtypes = [ctypes.c_char_p, _P, _I]
 _lib.gnf4_call_stats_get.restype = _I
 _lib.gnf4_call_stats_name.argtypes = [_I]
 _lib.gnf4_call_stats_name.restype = ctypes.c_char_p
-for _name in ("gnf4_device_errors", "gnf4_route_permute", "gnf4_route_permute_static", "gnf4_route_topk_permute",
+_lib.gnf4_moe_decode_workspace_bytes.argtypes = [_I, _I, _I, _I]
+_lib.gnf4_moe_decode_workspace_bytes.restype = _SZ
+for _name in ("gnf4_moe_decode_nf4", "gnf4_moe_decode_mxfp4"):
+    getattr(_lib, _name).argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.gnf4_swiglu_ckpt8.argtypes = [_P, _I, _I, _P, _P, _P, _P, _P]
+_lib.gnf4_swiglu_ckpt8_backward.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P]
+_lib.gnf4_combine_backward.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]
+_lib.gnf4_route_topk_backward.argtypes = [_P, _P, _P, _I, _I, _I, _P, _P]
+for _name in ("gnf4_moe_decode_nf4", "gnf4_moe_decode_mxfp4", "gnf4_swiglu_ckpt8", "gnf4_swiglu_ckpt8_backward",
+              "gnf4_combine_backward", "gnf4_route_topk_backward",
+              "gnf4_device_errors", "gnf4_route_permute", "gnf4_route_permute_static", "gnf4_route_topk_permute",
               *_GROUPED, "gnf4_combine", "gnf4_quantize_mxfp8", "gnf4_grouped_gemm_w4a8",
               "gnf4_quantize_mxfp8_split", "gnf4_grouped_gemm_w4a8x2",
               "gnf4_quantize_mxfp4_act", "gnf4_grouped_gemm_w4a4", "gnf4_selftest_bounded_wait",
@@ -400,3 +410,75 @@ def grouped_gemm_w4a4(a_blocks, a_scales, w, w_scales, y, offsets=None, counts=N
     M = a_blocks.shape[0]
     _check(_lib.gnf4_grouped_gemm_w4a4(_ptr(a_blocks), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets),
                                        _ptr(counts), E, N, 2 * K2, M, _ptr(y), _stream(stream)))
+
+
+# ---------------------------------------------------------------- whole layer for a few tokens
+
+
+def moe_decode_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
+    """Bytes of the workspace moe_decode_* needs (zero-filled once before its first use)."""
+    return int(_lib.gnf4_moe_decode_workspace_bytes(T, k, H, I))
+
+
+def _moe_decode(fn, x, w_gate_up, scales_gate_up, w_down, scales_down, logits, topk_ids, topk_weights, out, workspace,
+                router_w, bias, stream):
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    H, I = x.shape[1], w_gate_up.shape[1] // 2
+    _check(fn(_ptr(x), _ptr(router_w), _ptr(bias), _ptr(logits), T, E, k, H, I, _ptr(w_gate_up), _ptr(scales_gate_up),
+              _ptr(w_down), _ptr(scales_down), _ptr(topk_ids), _ptr(topk_weights), _ptr(out), _ptr(workspace),
+              workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def moe_decode_nf4(x, w_gate_up, absmax_gate_up, w_down, absmax_down, logits, topk_ids, topk_weights, out, workspace,
+                   router_w=None, bias=None, stream=None):
+    """A whole routed layer for T <= 8 tokens in one launch: out [T, H] from x [T, H] and the NF4 stacks
+    w_gate_up [E, 2I, H/2], w_down [E, H, I/2].  With router_w [E, H] the logits [T, E] are computed (and written),
+    else read; topk_ids and topk_weights [T, k] are outputs.  workspace: a zeroed uint8 tensor of
+    moe_decode_workspace_bytes(T, k, H, I) bytes, left zeroed where it has to be."""
+    _moe_decode(_lib.gnf4_moe_decode_nf4, x, w_gate_up, absmax_gate_up, w_down, absmax_down, logits, topk_ids,
+                topk_weights, out, workspace, router_w, bias, stream)
+
+
+def moe_decode_mxfp4(x, w_gate_up, scales_gate_up, w_down, scales_down, logits, topk_ids, topk_weights, out, workspace,
+                     router_w=None, bias=None, stream=None):
+    """moe_decode_nf4 on MXFP4 stacks (e8m0 scales [E, 2I, H/32] and [E, H, I/32])."""
+    _moe_decode(_lib.gnf4_moe_decode_mxfp4, x, w_gate_up, scales_gate_up, w_down, scales_down, logits, topk_ids,
+                topk_weights, out, workspace, router_w, bias, stream)
+
+
+# ---------------------------------------------------------------- training
+
+
+def swiglu_ckpt8(gate_up, h, codes, scales, num_rows=None, stream=None):
+    """h [M, I] = silu(gate) * up of gate_up [M, 2I], and gate_up's 8-bit checkpoint: codes uint8 [M, 2I] (e4m3),
+    scales uint8 [M, 2I/32] (e8m0).  num_rows: int32 device tensor; rows past num_rows[0] are left alone."""
+    M, I = h.shape
+    _check(_lib.gnf4_swiglu_ckpt8(_ptr(gate_up), M, I, _ptr(num_rows), _ptr(h), _ptr(codes), _ptr(scales),
+                                  _stream(stream)))
+
+
+def swiglu_ckpt8_backward(dh, codes, scales, d_gate_up, num_rows=None, sorted_to_flat=None, flat_to_sorted=None,
+                          weights=None, d_weights=None, h=None, stream=None):
+    """d_gate_up [M, 2I] from dh [M, I] (without the router weights) and the 8-bit checkpoint; with the routing also
+    the weights' factor and d_weights [T, k]; h [M, I]: recomputed activations (optional)."""
+    M, I = dh.shape
+    _check(_lib.gnf4_swiglu_ckpt8_backward(_ptr(dh), _ptr(codes), _ptr(scales), _ptr(num_rows), _ptr(sorted_to_flat),
+                                           _ptr(flat_to_sorted), _ptr(weights), M, I, _ptr(d_gate_up), _ptr(h),
+                                           _ptr(d_weights), _stream(stream)))
+
+
+def combine_backward(dout, sorted_to_flat, flat_to_sorted, dy, k, weights=None, y=None, d_weights=None, stream=None):
+    """dy [T*k, N] = weights * dout [T, N] in sorted rows (weights None: a gather; rows without a pair zero), and
+    d_weights [T, k] = <dout, y> (needs y [T*k, N])."""
+    T, N = dout.shape
+    _check(_lib.gnf4_combine_backward(_ptr(dout), _ptr(y), _ptr(sorted_to_flat), _ptr(flat_to_sorted), _ptr(weights),
+                                      T, k, N, _ptr(dy), _ptr(d_weights), _stream(stream)))
+
+
+def route_topk_backward(topk_ids, topk_weights, d_weights, d_logits, stream=None):
+    """d_logits [T, E] of the softmax over each token's selected logits (0 for the other experts)."""
+    T, k = topk_ids.shape
+    E = d_logits.shape[1]
+    _check(_lib.gnf4_route_topk_backward(_ptr(topk_ids), _ptr(topk_weights), _ptr(d_weights), T, k, E, _ptr(d_logits),
+                                         _stream(stream)))

@@ -500,6 +500,143 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
                          void *out, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* A whole routed layer for a few tokens (decode)                      */
+/* ------------------------------------------------------------------ */
+
+/* Router, selection, both projections, activation and weighted sum of a
+ * routed layer in one launch, for T <= 8 tokens (grouped-nf4-gemm index.json,
+ * problems_solved[5]: the decode tail folded into fewer launches).  For every
+ * token t:
+ *     logits[t, e] = sum_i x[t, i] router_w[e, i]          (fp32),
+ *     topk_ids, topk_weights: as gnf4_route_topk_permute selects and weighs
+ *       them from logits and bias (ties to the lower expert, NaN last, softmax
+ *       over the k selected raw logits),
+ *     h[t, j]  = silu(G_e x[t]) * (U_e x[t]),  e = topk_ids[t, j], G_e / U_e
+ *       rows [0, I) / [I, 2I) of w_gate_up[e],
+ *     out[t]   = sum_j topk_weights[t, j] * (D_e h[t, j]),  D_e = w_down[e].
+ * Sums are fp32.  Rounded to bf16: topk_weights[t, j] * h[t, j], out, and the
+ * 16 NF4 codes (after a scaling that minimises their error; absmax is applied
+ * in fp32); MXFP4 weights are exact.  Two calls with the same inputs give the
+ * same bits.
+ *   x             bf16 [T, H];
+ *   router_w      bf16 [E, H], or NULL: logits are then an input;
+ *   bias          fp32 [E] or NULL: added for the selection only;
+ *   logits        fp32 [T, E]: OUT with router_w, else IN;
+ *   w_gate_up     uint8 [E, 2I, H/2] with its scales (fp32 absmax [E, 2I, H/64]
+ *                 or e8m0 [E, 2I, H/32]); w_down uint8 [E, H, I/2] with its
+ *                 scales ([E, H, I/64] or [E, H, I/32]);
+ *   topk_ids      int32 [T, k] OUT; topk_weights fp32 [T, k] OUT;
+ *   out           bf16 [T, H] OUT;
+ *   workspace     device memory of gnf4_moe_decode_workspace_bytes(T, k, H, I)
+ *                 bytes or more, zero-filled once by the caller before its
+ *                 first use.  Every call that ends without a device error
+ *                 leaves its counters zero, so it may be used again by calls
+ *                 of any shape it is large enough for, and captured in a
+ *                 graph.  After a device error zero it again.  Calls
+ *                 that may overlap on the GPU (two streams, two graphs) need a
+ *                 workspace each.
+ * Rules: 0 <= T <= 8, 1 <= E <= 1024, 1 <= k <= min(E, 32), H and I multiples
+ * of 64 (NF4) or 32 (MXFP4), H >= that, T*H <= 57344 and H <= 57344,
+ * that <= I <= 65536.  x, router_w, w_gate_up, w_down, out and workspace
+ * 16-byte aligned.  T == 0 does nothing.  Every pointer must be memory of the
+ * current device (or managed).  The launch is cooperative: one CTA on every
+ * SM, with bounded waits between them. */
+size_t gnf4_moe_decode_workspace_bytes(int T, int k, int H, int I);
+gnf4_status gnf4_moe_decode_nf4(const void *x, const void *router_w, const float *bias, float *logits, int T, int E,
+                                int k, int H, int I, const uint8_t *w_gate_up, const float *absmax_gate_up,
+                                const uint8_t *w_down, const float *absmax_down, int32_t *topk_ids,
+                                float *topk_weights, void *out, void *workspace, size_t workspace_bytes,
+                                void *stream);
+gnf4_status gnf4_moe_decode_mxfp4(const void *x, const void *router_w, const float *bias, float *logits, int T, int E,
+                                  int k, int H, int I, const uint8_t *w_gate_up, const uint8_t *scales_gate_up,
+                                  const uint8_t *w_down, const uint8_t *scales_down, int32_t *topk_ids,
+                                  float *topk_weights, void *out, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Training: gate_up kept in 8 bits, backward of combine and router    */
+/* ------------------------------------------------------------------ */
+
+/* The calls between the GEMMs of a training step on frozen expert stacks:
+ *     forward   gate_up = gnf4_grouped_gemm_*(x_sorted);
+ *               gnf4_swiglu_ckpt8 -> h and the 8-bit checkpoint of gate_up;
+ *               y = gnf4_grouped_gemm_*(h); out = gnf4_combine(y).
+ *     backward  gnf4_combine_backward(dout, weights = NULL) -> dout in sorted
+ *               rows; dh = gnf4_grouped_dgrad_*(that, w_down);
+ *               gnf4_swiglu_ckpt8_backward(dh) -> d_gate_up and d_weights;
+ *               dx_sorted = gnf4_grouped_dgrad_*(d_gate_up, w_gate_up);
+ *               dx = gnf4_combine(dx_sorted, weights all 1);
+ *               gnf4_route_topk_backward(d_weights) -> d_logits.
+ * Between the passes only the codes, the scales and the routing are kept:
+ * neither gate_up, h nor y.  (The pages name the dgrad and the checkpointed
+ * layer but no 8-bit form: this is a reading.)
+ *
+ * gnf4_swiglu_ckpt8, for every row r < num_rows:
+ *     h[r, i] = silu(gate_up[r, i]) * gate_up[r, I + i]         (fp32, one rounding to bf16),
+ *     codes / scales[r]: the 2I values as MXFP8 with X = max(floor(log2(max|v|)) - 7, -127)
+ *       per 32 consecutive values, scale byte X + 127, code = v * 2^-X rounded to
+ *       the nearest e4m3 value, ties to even: nothing saturates.  Non-finite
+ *       values become the e4m3 NaN and do not enter the block's maximum.
+ *   gate_up bf16 [M, 2I] (gate values first); num_rows int32 [1] on the device
+ *   or NULL (= M; offsets + E of the routing is what a sorted batch passes):
+ *   rows at and past it are neither read nor written; h bf16 [M, I] OUT; codes uint8
+ *   [M, 2I] OUT; scales uint8 [M, 2I/32] OUT.
+ * Rules: M >= 0, I >= 32 and I % 32 == 0, M*I <= 2^40; gate_up, h and codes
+ * 16-byte aligned. */
+gnf4_status gnf4_swiglu_ckpt8(const void *gate_up, int M, int I, const int32_t *num_rows, void *h, uint8_t *codes,
+                              uint8_t *scales, void *stream);
+
+/* Backward of the above from the 8-bit values g, u of a row, s = 1 / (1 + exp(-g)),
+ * with f = sorted_to_flat[r] the row's pair and w = weights[f] (1 if weights is NULL):
+ *     d_gate_up[r, i]     = w * dh[r, i] * u * s * (1 + g * (1 - s)),
+ *     d_gate_up[r, I + i] = w * dh[r, i] * g * s,
+ *     h[r, i]             = g * s * u                    (optional; without w),
+ *     d_weights[f]        = sum_i dh[r, i] * g * s * u   (optional; fp32).
+ * dh is the gradient through the down projection without w; d_weights is then
+ * the gradient of the router weights (<dout, y> = <dh, h>), y is not needed.
+ *   dh bf16 [M, I]; codes, scales, num_rows as written / passed above;
+ *   sorted_to_flat int32 [M] or NULL: with it, rows whose pair is outside
+ *   [0, M) are left alone as rows past num_rows are; flat_to_sorted int32 [M]
+ *   or NULL: needed with d_weights, whose entry is 0 for a pair without a row
+ *   (flat_to_sorted outside [0, num_rows)); weights fp32 [M] (the [T, k]
+ *   router weights) or NULL; d_gate_up bf16 [M, 2I] OUT; h bf16 [M, I] OUT or
+ *   NULL; d_weights fp32 [M] OUT or NULL.  weights and d_weights need
+ *   sorted_to_flat.  The two permutations are inverse to each other, as the
+ *   routing calls write them.  Outputs may not overlap inputs.
+ * Rules as gnf4_swiglu_ckpt8; dh, codes, d_gate_up and h 16-byte aligned. */
+gnf4_status gnf4_swiglu_ckpt8_backward(const void *dh, const uint8_t *codes, const uint8_t *scales,
+                                       const int32_t *num_rows, const int32_t *sorted_to_flat,
+                                       const int32_t *flat_to_sorted, const float *weights, int M, int I,
+                                       void *d_gate_up, void *h, float *d_weights, void *stream);
+
+/* Backward of gnf4_combine, with f = sorted_to_flat[r]:
+ *     dy[r, n]     = weights[f] * dout[f / k, n]          (weights NULL: 1, a plain gather),
+ *     d_weights[f] = sum_n dout[f / k, n] * y[r, n]       (optional; fp32).
+ * Rows whose pair is outside [0, T*k) are written as zeros (as the routing
+ * pads x_sorted); a pair whose flat_to_sorted is outside [0, T*k) gets
+ * d_weights 0.
+ *   dout bf16 [T, N]; y bf16 [T*k, N] or NULL (needed with d_weights);
+ *   sorted_to_flat int32 [T*k]; flat_to_sorted int32 [T*k] or NULL (needed with
+ *   d_weights); weights fp32 [T, k] or NULL; dy bf16 [T*k, N] OUT; d_weights
+ *   fp32 [T, k] OUT or NULL.
+ * Rules: T >= 0, k >= 1, T*k < 2^31, N >= 8 and N % 8 == 0; dout, y and dy
+ * 16-byte aligned. */
+gnf4_status gnf4_combine_backward(const void *dout, const void *y, const int32_t *sorted_to_flat,
+                                  const int32_t *flat_to_sorted, const float *weights, int T, int k, int N, void *dy,
+                                  float *d_weights, void *stream);
+
+/* Backward of the router epilogue's softmax over the selected logits:
+ *     d_logits[t, topk_ids[t, j]] = p_j * (d_weights[t, j] - sum_i p_i d_weights[t, i]),
+ *       p = topk_weights[t],
+ * and 0 for every other expert (the bias gets no gradient: it moves the
+ * selection only).  An id outside [0, E) keeps its place in the sum and
+ * writes nothing; equal ids of a token add up.
+ *   topk_ids int32 [T, k], topk_weights and d_weights fp32 [T, k], d_logits
+ *   fp32 [T, E] OUT.  Rules: T >= 0, 1 <= E <= 4096, 1 <= k <= min(E, 32). */
+gnf4_status gnf4_route_topk_backward(const int32_t *topk_ids, const float *topk_weights, const float *d_weights,
+                                     int T, int k, int E, float *d_logits, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Decode checks (test support)                                        */
 /* ------------------------------------------------------------------ */
 
