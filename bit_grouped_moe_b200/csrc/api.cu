@@ -1094,8 +1094,8 @@ static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w,
   GNF4_TRY(check_local_ptr(topk_ids, "topk_ids", 4));
   GNF4_TRY(check_local_ptr(topk_weights, "topk_weights", 4));
   GNF4_TRY(check_local_ptr(out, "out", 16));
-  size_t count_at, part_at, h_at;
-  const size_t need = moe_decode_workspace(T, k, H, I, &count_at, &part_at, &h_at);
+  size_t at[4];
+  const size_t need = moe_decode_workspace(T, k, H, I, at);
   if (workspace_bytes < need)
     return fail(GNF4_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
                 need);
@@ -1113,12 +1113,30 @@ static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w,
   p.topk_ids = topk_ids, p.topk_weights = topk_weights;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.sync = reinterpret_cast<unsigned*>(ws);
-  p.unit_count = reinterpret_cast<unsigned*>(ws + count_at);
-  p.part = reinterpret_cast<float*>(ws + part_at);
-  p.hbuf = reinterpret_cast<__nv_bfloat16*>(ws + h_at);
+  p.hmax = reinterpret_cast<unsigned*>(ws + at[0]);
+  p.unit_count = reinterpret_cast<unsigned*>(ws + at[1]);
+  p.part = reinterpret_cast<float*>(ws + at[2]);
+  p.hbuf = reinterpret_cast<float*>(ws + at[3]);
   p.err = d->err;
   p.T = T, p.E = E, p.k = k, p.H = H, p.I = I;
-  cudaError_t e = launch_moe_decode(fmt, p, d->num_sms, as_stream(stream));
+  CUtensorMap map1, map2;
+  {
+    auto fn = encode_fn();
+    if (!fn) return fail(GNF4_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    const cuuint64_t r1 = (cuuint64_t)(H / 2), r2 = (cuuint64_t)(I / 2);
+    cuuint64_t dims1[4] = {r1, (cuuint64_t)I, 2, (cuuint64_t)E}, dims2[3] = {r2, (cuuint64_t)H, (cuuint64_t)E};
+    cuuint64_t strides1[3] = {r1, (cuuint64_t)I * r1, 2 * (cuuint64_t)I * r1}, strides2[2] = {r2, (cuuint64_t)H * r2};
+    cuuint32_t box1[4] = {64, 16, 2, 1}, box2[3] = {64, 32, 1}, estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(&map1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(w_gate_up), dims1, strides1, box1, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS)
+      r = fn(&map2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w_down), dims2, strides2, box2, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(GNF4_ERR_CUDA, "expert stack tensor map encode failed (CUresult %d)", (int)r);
+  }
+  cudaError_t e = launch_moe_decode(fmt, map1, map2, p, d->num_sms, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "MoE decode launch");
   note_launch(kPathOther);
   return GNF4_OK;
@@ -1130,8 +1148,8 @@ size_t gnf4_moe_decode_workspace_bytes(int T, int k, int H, int I) {
   if (T < 1 || T > kMoeDecodeMaxTokens || k < 1 || k > kMaxRouterTopK || H < 32 || I < 32 || I > 65536 ||
       H > kMoeDecodeMaxTH)
     return 0;
-  size_t a, b, c;
-  return moe_decode_workspace(T, k, H, I, &a, &b, &c);
+  size_t at[4];
+  return moe_decode_workspace(T, k, H, I, at);
 }
 
 gnf4_status gnf4_moe_decode_nf4(const void* x, const void* router_w, const float* bias, float* logits, int T, int E,

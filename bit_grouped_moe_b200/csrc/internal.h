@@ -187,14 +187,19 @@ struct MoeDecodeArgs {
   float* topk_weights;            // [T, k]
   __nv_bfloat16* out;             // [T, H]
   unsigned* sync;                 // workspace: barrier words, zero between calls
-  unsigned* unit_count;           // workspace: [H/16], zero between calls
+  unsigned* hmax;                 // workspace: largest |h| per pair (fp32 bits), zero between calls
+  unsigned* unit_count;           // workspace: [H/32], zero between calls
   float* part;                    // workspace: partial sums of output tiles split between CTAs
-  __nv_bfloat16* hbuf;            // workspace: [T*k, I padded to 128], in MMA fragment order
+  float* hbuf;                    // workspace: [T*k, I padded to 128], in MMA fragment order
   unsigned* err;
   int T, E, k, H, I;
 };
-size_t moe_decode_workspace(int T, int k, int H, int I, size_t* count_at, size_t* part_at, size_t* h_at);
-cudaError_t launch_moe_decode(int fmt, const MoeDecodeArgs& p, int num_sms, cudaStream_t stream);
+// Bytes in all; at[0..3]: where hmax, unit_count, part and hbuf begin (sync at 0).
+size_t moe_decode_workspace(int T, int k, int H, int I, size_t* at);
+// map1: w1 as [E][gate, up][I][H/2] in boxes of 64 bytes x 16 rows x both; map2: w2 as [E][H][I/2] in boxes of
+// 64 bytes x 32 rows; both with the 64-byte swizzle and zero fill.
+cudaError_t launch_moe_decode(int fmt, const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p,
+                              int num_sms, cudaStream_t stream);
 
 // selftest.cu: one bounded wait on a barrier nothing arrives on
 cudaError_t launch_bounded_wait_probe(unsigned* err, long long limit_cycles, cudaStream_t stream);

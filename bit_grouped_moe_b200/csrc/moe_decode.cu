@@ -9,38 +9,50 @@
 //   0 router: a CTA computes the logits of its experts (skipped when given);
 //   1 every CTA selects the top-k of every token itself (a warp per token) and
 //     lists the hit experts: cheaper than a barrier around one CTA doing it;
-//   2 gate_up + SwiGLU: work unit = 8 gate rows and the 8 matching up rows of
-//     a hit expert, one m16 tile, so a lane ends with both halves of a value;
-//   3 down + combine: work unit = 16 output rows over ALL hit experts: the
+//   2 gate_up + SwiGLU: work unit = 16 gate rows and the 16 matching up rows
+//     of a hit expert, two m16 tiles of 8 + 8, so a lane ends with both halves
+//     of a value;
+//   3 down + combine: work unit = 32 output rows over ALL hit experts: the
 //     router weight is folded into h, so the weighted sum over the experts is
 //     the same fp32 accumulator and no per-expert output exists.
-// A unit's K (phase 3: hit experts x K) is cut in items of 128 k; the item
-// sequence of a CTA is divided evenly over its 16 warps and each warp streams
-// a contiguous range, so every warp has the same number of 1 KB loads
-// whatever the shapes are.  A warp that covers a whole unit finishes it in
-// registers; split units are added through shared memory in warp order.  In
-// phase 3 the item sequence is also divided evenly over the CTAs (16-row
-// units would leave up to 39% of the SMs idle); a unit split between CTAs is
-// added by the last CTA to finish it, in CTA order, from partial sums in the
-// workspace.  Every sum has a fixed order: outputs do not depend on timing.
+// A unit's K (phase 3: hit experts x K) is cut in items of 32 rows x 128 k
+// (2 KB of codes); the item sequence of a CTA is divided evenly over its 16
+// warps and each warp streams a contiguous range.  A warp that covers a whole
+// unit finishes it in registers; split units are added through shared memory
+// in warp order.  In phase 3 the item sequence is also divided evenly over the
+// CTAs (whole units would leave up to half of the SMs idle); a unit split
+// between CTAs is added by the last CTA to finish it, in CTA order, from
+// partial sums in the workspace.  Every sum has a fixed order: outputs do not
+// depend on timing.
 //
-// MMA mapping (m16n8k16): A = decoded weights, B = activations, the MMA's 8
-// columns are the T tokens.  In phase 2 all tokens share B, whichever expert
-// they chose: products of tokens that did not choose it are computed (the
-// MMA has the columns anyway) and dropped.  x lies in shared memory in
-// fragment order.  In phase 3 lanes of tokens that did not choose the expert
-// hold zeros.
+// Loads: every warp has its own ring of TMA boxes (one instruction per item)
+// and issues them itself; nothing is shared between warps, so the ring needs
+// no empty barriers.  Plain loads of the same tiles are bound by the L1: 8
+// rows x 64 bytes touch 8 lines per instruction, and what shared memory leaves
+// of the L1 (28 KB) caps the bytes in flight (1.8 TB/s at T = 8, H = 7168).
+// Scales come by plain loads, one row per lane and four items at a time.
 //
-// Decode: the per-lane pair table of the grouped GEMV (a byte = one PRMT and
-// one shared load).
-//   MXFP4: e2m1 x 2^(e-127) is exact in bf16 (a power-of-two multiply per pair).
-//   NF4: a lane's 16 codes of a 64-block feed four MMAs whose fp32 result is
-//     multiplied by absmax, so absmax is not rounded.  The codes are rounded
-//     to bf16 after a multiplication by kNf4Gain, undone in fp32: the gain is
-//     the one in [1, 2) that minimises the rounding error of the 16 codes
-//     (rms 0.063% instead of 0.106%).
-// Rounded to bf16: h times its router weight (once, from fp32), and out.
+// MMA mapping (m16n8k16, fp16 operands, fp32 sums): A = weight codes, B =
+// activations.  A lane's codes of one scale block feed two (MXFP4) or four
+// (NF4) MMAs whose result is multiplied by the scale in fp32, so scales are not
+// rounded and not multiplied into the weights one by one.  e2m1 is exact in
+// fp16, NF4 codes are within 2^-12.  Activations are scaled by the power of two
+// that puts the largest of a token's x (of a (token, expert) pair's h) in
+// [2^14, 2^15): 8-bit significands of x stay exact down to 2^-28 of it, h is
+// rounded to 11 bits.  The largest of h is known when phase 2 ends (an integer
+// maximum in the workspace), so phase 2 leaves h in fp32 and phase 3 rounds it.
+//   Phase 2: the MMA's 8 columns are the T tokens, whichever expert they
+// chose; products of tokens that did not choose it are computed (the MMA has
+// the columns anyway) and dropped.  x lies in shared memory in fragment order.
+//   Phase 3: columns as in phase 2; a lane fetches its part of h for the next
+// item while it works on this one.
+//
+// Decode: MXFP4 converts a byte to an fp16 pair with one instruction
+// (cvt.rn.f16x2.e2m1x2: half a cycle per SM, measured).  NF4 looks a byte up in
+// the per-lane pair table of the grouped GEMV (one PRMT and one shared load).
+// Rounded to 16 bits apart from that: out, once.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -54,43 +66,79 @@ constexpr int kMaxT = kMoeDecodeMaxTokens;
 constexpr int kMaxPairs = kMaxT * kMaxRouterTopK;  // hit experts never exceed this
 constexpr int kMaxGrid = 160;                      // CTAs (one per SM; B200 has 148)
 constexpr int kDK = 128;                           // k per item
-constexpr int kStages = 4;                         // items in flight per warp
-constexpr float kNf4Gain = 1.43701171875f;
+constexpr int kItemBytes = 32 * kDK / 2;           // one TMA box
+constexpr int kMaxStages = 2;                      // items in flight per warp (4: 5.1 instead of 6.6 TB/s, loads alone)
+constexpr uint32_t kMaxWindow = 227 * 1024;        // dynamic shared memory of a CTA
 
-// Shared memory: the pair table needs a 64 KB boundary of the shared window.
-// x in fragment order goes below it: it starts at the first boundary that
-// leaves room (0x10000 or 0x20000).  Everything else lies above the table.
-struct Tables {
-  float part[kWarps][2][32][4];       // partial sums: [0] of a unit begun by an earlier warp, [1] of one begun here
-  float wt[kMaxPairs][kMaxT];         // router weight of (hit expert, token), 0 if not routed
-  short row[kMaxPairs][kMaxT];        // row of hbuf of (hit expert, token), -1 if not routed
-  short expert[kMaxPairs];            // hit expert ids, ascending
-  uint32_t hit[kMaxExperts / 32];     // bit per expert
-  float red[kWarps][kMaxT];           // router products per warp
-  int sel_id[kMaxT][kMaxRouterTopK];
-  float sel_p[kMaxT][kMaxRouterTopK];
+struct Route {
+  short row[kMaxPairs][kMaxT];  // pair = row of h of (hit expert, token); ~(a pair of the expert) if not routed
+  short expert[kMaxPairs];      // hit expert ids, ascending
+  uint32_t hit[kMaxExperts / 32];
+  short sel_id[kMaxPairs];      // by pair
+  float sel_p[kMaxPairs];
+};
+struct Work {
+  uint64_t full[kWarps][kMaxStages];
+  float red[kWarps][kMaxT];     // router products per warp
+  uint32_t xmax[kMaxT];         // largest finite |x| of a token (fp32 bits)
+  float hscale[kMaxPairs];      // scale of a pair's fp16 h
   int nhit;
+  int tiny;                     // a pair's h lies below 2^kTinyExp throughout
   int ok;
+  int abort;
+};
+// Sums in units of scaled activations overflow before the true sum does; below this exponent of the largest
+// activation (a true sum of 2^50 could) blocks are brought back to true units before they are added.
+constexpr int kTinyExp = -64;
+// fp32 bits of the largest |v| -> the scale 2^(14 - e), its inverse, and whether e < kTinyExp; e at least 15 - 127.
+__device__ __forceinline__ uint32_t exp_field(uint32_t top) { return max(top >> 23, 15u); }
+__device__ __forceinline__ float scale_up(uint32_t top) { return __uint_as_float((268u - exp_field(top)) << 23); }
+__device__ __forceinline__ float scale_down(uint32_t top) { return __uint_as_float((exp_field(top) - 14u) << 23); }
+__device__ __forceinline__ bool is_tiny(uint32_t top) { return top != 0u && top < (uint32_t)(127 + kTinyExp) << 23; }
+
+// Offsets in the dynamic shared window.  x in fragment order (in phase 3: 64
+// bytes of h per lane), Route, Work and MXFP4's scale scratch first; NF4's pair table at a 64 KB boundary (0x10000, or
+// 0x20000 where x needs the room); then the rings.
+struct Plan {
+  uint32_t route, work, scratch, table, ring, total;
+  int stages;
 };
 
 constexpr uint32_t kWindow = 0x400;  // start of the dynamic shared window that the host's layout assumes
-constexpr int kSyncBytes = 256;      // workspace: words 0, 1 = grid barriers, 2 = CTAs that have left
-
+// A warp's scratch: the fp32 scales of four items.  MXFP4 [4][32 rows][4], 2 KB of its own; NF4 [4][32][2] in the
+// unused upper halves of eight entries of the pair table, 16 rows to an entry.
+constexpr int kScratchStride = 2048, kScratchItem = 512;  // per warp, per item
 template <int FMT>
+__device__ __forceinline__ constexpr int scratch_row(int r) {
+  return FMT == 0 ? (r >> 4) * 256 + (r & 15) * 8 : 16 * r;
+}
+constexpr uint32_t kHBytes = kThreads * 64;     // phase 3: h of one item
+constexpr int kSyncBytes = 256;      // workspace: words 0, 1 = grid barriers, 2 = CTAs that have left; then hmax
+
+// NF4 pairs as fp16, one copy per lane, 256 bytes per entry.
 __device__ __forceinline__ void build_table(uint32_t* lut, int tid) {
-  for (int i = tid; i < 256 * 32; i += kThreads) {
-    const uint32_t b = (uint32_t)i >> 5, l = (uint32_t)i & 31u;
-    float lo, hi;
-    if (FMT == 0) {
-      lo = kNf4Code[b >> 4] * kNf4Gain;
-      hi = kNf4Code[b & 15u] * kNf4Gain;
-    } else {
-      lo = e2m1_value(b & 15u);
-      hi = e2m1_value(b >> 4);
-    }
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    lut[b * 64u + l] = *reinterpret_cast<uint32_t*>(&v);
+  for (int i = tid; i < 256 * 8; i += kThreads) {
+    const uint32_t b = (uint32_t)i >> 3;
+    __half2 h = __floats2half2_rn(kNf4Code[b >> 4], kNf4Code[b & 15u]);
+    const uint32_t v = *reinterpret_cast<uint32_t*>(&h);
+    *reinterpret_cast<uint4*>(lut + b * 64u + 4u * ((uint32_t)i & 7u)) = make_uint4(v, v, v, v);
   }
+}
+
+// D (16x8 fp32) = A (16x16 f16, row) x B (16x8 f16, col), or += in the second form.
+__device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Byte j of `word` selects the entry; `lanesel` holds 4*lane in byte 0 and the table's 64 KB base in byte 2.
@@ -100,19 +148,41 @@ __device__ __forceinline__ uint32_t lookup(uint32_t word, uint32_t lanesel, uint
   return v;
 }
 
-// Offset inside a 128-k item of the 8 consecutive k that chunk c (0..3) of lane column t holds.
+// Eight e2m1 codes to four fp16 pairs (k0,k1) .. (k6,k7), exactly.
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&p)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}\n"
+      : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+      : "r"(w));
+}
+// Fragment order of activations: chunk c (0..3) of lane column t holds 8
+// consecutive k of a 128-k item, starting at chunk_k; chunk_of is the inverse.
 template <int FMT>
 __device__ __forceinline__ int chunk_k(int t, int c) {
-  return FMT == 0 ? 64 * (c >> 1) + 16 * t + 8 * (c & 1) : 32 * t + 8 * c;
+  return FMT == 0 ? 64 * (c >> 1) + 16 * t + 8 * (c & 1) : 32 * c + 8 * t;
+}
+template <int FMT>  // k inside the item, a multiple of 8 -> 4 * c + t
+__device__ __forceinline__ int chunk_of(int k) {
+  return FMT == 0 ? 4 * (2 * (k >> 6) + ((k >> 3) & 1)) + ((k & 63) >> 4) : 4 * (k >> 5) + ((k >> 3) & 3);
+}
+__device__ __forceinline__ unsigned atom_add_acq_rel(unsigned* p, unsigned v) {
+  unsigned o;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(o) : "l"(p), "r"(v) : "memory");
+  return o;
 }
 
-// All CTAs of the grid meet (cooperative launch: they are all resident).
-// Bounded: false after the wait limit, with the timeout flagged.
-__device__ __forceinline__ bool grid_barrier(unsigned* ctr, unsigned* err, int* ok) {
+// All CTAs of the grid meet (cooperative launch: they are all resident).  The
+// release is cumulative over the block barrier before it, the acquire over the
+// one after it (a full fence on either side cost 1 to 4 us).
+__device__ __forceinline__ void grid_arrive(unsigned* ctr) {
   __syncthreads();
+  if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
+}
+// Bounded: false after the wait limit, with the timeout flagged.
+__device__ __forceinline__ bool grid_wait(unsigned* ctr, unsigned* err, int* ok) {
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(ctr, 1u);
     const long long t0 = clock64();
     int good = 1;
     while (true) {
@@ -125,7 +195,6 @@ __device__ __forceinline__ bool grid_barrier(unsigned* ctr, unsigned* err, int* 
         break;
       }
     }
-    __threadfence();
     *ok = good;
   }
   __syncthreads();
@@ -144,35 +213,53 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
   return acc;
 }
 
-__device__ __forceinline__ void router_product(const MoeDecodeArgs& p, Tables& s, int tid) {
-  const int warp = tid >> 5, lane = tid & 31;
-  const int H8 = p.H / 8;
+// The CTA's experts are blockIdx + i * grid, each the work of `wpe` warps (E <= 1024: at most 7 a CTA).
+struct RouterPart {
+  int wpe, e, first;
+  uint4 w;  // this thread's first chunk, loaded early
+  __device__ __forceinline__ RouterPart(const MoeDecodeArgs& p, int tid) {
+    const int per_cta = (p.E + (int)gridDim.x - 1) / (int)gridDim.x, warp = tid >> 5;
+    wpe = per_cta <= 1 ? 16 : per_cta <= 2 ? 8 : per_cta <= 4 ? 4 : 2;
+    e = blockIdx.x + (warp / wpe) * (int)gridDim.x;
+    first = (warp % wpe) * 32 + (tid & 31);
+    w = make_uint4(0u, 0u, 0u, 0u);
+    if (p.router_w != nullptr && e < p.E && first < p.H / 8)
+      w = ldg_nc_u128(reinterpret_cast<const uint4*>(p.router_w) + (size_t)e * (p.H / 8) + first);
+  }
+};
+
+// logits of the CTA's experts (TP >= T tokens).
+template <int TP>
+__device__ __forceinline__ void router_product(const MoeDecodeArgs& p, Work& s, const RouterPart& part, int tid) {
+  const int warp = tid >> 5, lane = tid & 31, H8 = p.H / 8, wpe = part.wpe, e = part.e;
   const uint4* x = reinterpret_cast<const uint4*>(p.x);
-  for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
+  float acc[TP];
+#pragma unroll
+  for (int t = 0; t < TP; ++t) acc[t] = 0.f;
+  if (e < p.E) {
     const uint4* w = reinterpret_cast<const uint4*>(p.router_w) + (size_t)e * H8;
-    float acc[kMaxT];
+#pragma unroll 2
+    for (int i = part.first; i < H8; i += wpe * 32) {
+      const uint4 wv = i == part.first ? part.w : ldg_nc_u128(w + i);
+      uint4 xv[TP];
 #pragma unroll
-    for (int t = 0; t < kMaxT; ++t) acc[t] = 0.f;
-    for (int i = tid; i < H8; i += kThreads) {
-      const uint4 wv = ldg_nc_u128(w + i);
+      for (int t = 0; t < TP; ++t) xv[t] = __ldg(x + (size_t)min(t, p.T - 1) * H8 + i);
 #pragma unroll
-      for (int t = 0; t < kMaxT; ++t)
-        if (t < p.T) acc[t] = dot8(wv, ldg_u128(x + (size_t)t * H8 + i), acc[t]);
+      for (int t = 0; t < TP; ++t) acc[t] = dot8(wv, xv[t], acc[t]);
     }
+  }
 #pragma unroll
-    for (int t = 0; t < kMaxT; ++t) {
-      if (t >= p.T) break;
+  for (int d = 16; d >= 1; d >>= 1)
 #pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], d);
-      if (lane == 0) s.red[warp][t] = acc[t];
-    }
-    __syncthreads();
-    if (tid < p.T) {
-      float v = 0.f;
-      for (int i = 0; i < kWarps; ++i) v += s.red[i][tid];
-      p.logits[(size_t)tid * p.E + e] = v;
-    }
-    __syncthreads();
+    for (int t = 0; t < TP; ++t) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], d);
+  if (lane == 0)
+#pragma unroll
+    for (int t = 0; t < TP; ++t) s.red[warp][t] = acc[t];
+  __syncthreads();
+  if (e < p.E && warp % wpe == 0 && lane < p.T) {
+    float v = 0.f;
+    for (int i = 0; i < wpe; ++i) v += s.red[warp + i][lane];
+    p.logits[(size_t)lane * p.E + e] = v;
   }
 }
 
@@ -185,44 +272,50 @@ __device__ __forceinline__ uint32_t score_key(float f) {
 }
 
 // One warp, one token: the k best of logit + bias (descending, ties to the
-// lower expert, NaN last) and the softmax of their raw logits, as the
-// router epilogue of the routing call.
-__device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Tables& s, int t, int lane) {
-  const float* row = p.logits + (size_t)t * p.E;
-  uint32_t key[kMaxExperts / 32];
+// lower expert, NaN last) and the softmax of their raw logits, as the router
+// epilogue of the routing call.  A lane holds the keys of N experts.
+template <int N>
+__device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Route& s, int t, int lane) {
+  const float* logits = p.logits + (size_t)t * p.E;
+  uint32_t key[N];
+  float raw[N];
 #pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) {
-    key[i] = 0u;
-    if (i * 32 >= p.E) continue;
+  for (int i = 0; i < N; ++i) {
     const int e = i * 32 + lane;
-    if (e < p.E) {
-      float v = __ldcg(row + e);
-      if (p.bias != nullptr) v += __ldg(p.bias + e);
-      key[i] = score_key(v);
-    }
+    raw[i] = e < p.E ? __ldcg(logits + e) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < p.E ? score_key(p.bias != nullptr ? raw[i] + __ldg(p.bias + e) : raw[i]) : 0u;
   }
   int mine = 0;
+  float l = -INFINITY;
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0u;
+    uint32_t best = key[0];
+    float value = raw[0];
     int at = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-      if (i * 32 >= p.E) break;
+    for (int i = 1; i < N; ++i)
       if (key[i] > best) {
         best = key[i];
+        value = raw[i];
         at = i;
       }
-    }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const unsigned id = __reduce_min_sync(0xffffffffu, best == top ? (unsigned)(at * 32 + lane) : 0xFFFFFFFFu);
-    if ((int)(id & 31u) == lane) {
+    const uint32_t who = __ballot_sync(0xffffffffu, best == top);
+    int owner = __ffs((int)who) - 1;
+    if (who & (who - 1u))  // equal scores: the lowest expert
+      owner = (int)(__reduce_min_sync(0xffffffffu, best == top ? (unsigned)(at * 32 + lane) : 0xFFFFFFFFu) & 31u);
+    const float v = __shfl_sync(0xffffffffu, value, owner);
+    const int row = __shfl_sync(0xffffffffu, at, owner);
 #pragma unroll
-      for (int i = 0; i < kMaxExperts / 32; ++i)
-        if (i == (int)(id >> 5)) key[i] = 0u;
+    for (int i = 0; i < N; ++i) key[i] = owner == lane && i == at ? 0u : key[i];
+    if (lane == j) {
+      mine = row * 32 + owner;
+      l = v;
     }
-    if (lane == j) mine = (int)id;
   }
-  const float l = lane < p.k ? __ldcg(row + mine) : -INFINITY;
   float m = l;  // a NaN logit makes every weight NaN
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
@@ -235,8 +328,8 @@ __device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Tables& s, i
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane < p.k) {
     const float w = ex / sum;
-    s.sel_id[t][lane] = mine;
-    s.sel_p[t][lane] = w;
+    s.sel_id[t * p.k + lane] = (short)mine;
+    s.sel_p[t * p.k + lane] = w;
     atomicOr(&s.hit[mine >> 5], 1u << (mine & 31));
     if (blockIdx.x == 0) {
       p.topk_ids[t * p.k + lane] = mine;
@@ -245,166 +338,201 @@ __device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Tables& s, i
   }
 }
 
-__device__ __forceinline__ void list_hits(const MoeDecodeArgs& p, Tables& s, int tid) {
+// Hit experts in ascending order, and the pair of every (hit expert, token).  All threads.
+__device__ __forceinline__ void list_hits(const MoeDecodeArgs& p, Route& s, int* nhit, int tid) {
   // rank of expert e = set bits below it
   auto rank = [&](int e) {
     int r = __popc(s.hit[e >> 5] & ((1u << (e & 31)) - 1u));
     for (int i = 0; i < (e >> 5); ++i) r += __popc(s.hit[i]);
     return r;
   };
-  const int words = (p.E + 31) / 32;
-  if (tid == 0) {
+  const int pairs = p.T * p.k;
+  for (int i = tid; i < pairs * kMaxT; i += kThreads) s.row[i / kMaxT][i % kMaxT] = -1;
+  if (tid == kThreads - 1) {
     int n = 0;
-    for (int i = 0; i < words; ++i) n += __popc(s.hit[i]);
-    s.nhit = n;
-  }
-  for (int e = tid; e < p.E; e += kThreads)
-    if ((s.hit[e >> 5] >> (e & 31)) & 1u) s.expert[rank(e)] = (short)e;
-  for (int i = tid; i < kMaxPairs * kMaxT; i += kThreads) {
-    s.wt[i / kMaxT][i % kMaxT] = 0.f;
-    s.row[i / kMaxT][i % kMaxT] = -1;
+    for (int i = 0; i < (p.E + 31) / 32; ++i) n += __popc(s.hit[i]);
+    *nhit = n;
   }
   __syncthreads();
-  for (int i = tid; i < p.T * p.k; i += kThreads) {
-    const int t = i / p.k, j = i - t * p.k;
-    const int r = rank(s.sel_id[t][j]);
-    s.wt[r][t] = s.sel_p[t][j];
-    s.row[r][t] = (short)i;
+  if (tid < pairs) {  // pairs <= 256
+    const int e = s.sel_id[tid], r = rank(e);
+    s.expert[r] = (short)e;  // the same value from every pair of the expert
+    s.row[r][tid / p.k] = (short)tid;
+  }
+  __syncthreads();
+  if (tid < *nhit) {
+    short any = 0;
+    for (int t = 0; t < p.T; ++t)
+      if (s.row[tid][t] >= 0) any = s.row[tid][t];
+    for (int t = 0; t < kMaxT; ++t)
+      if (s.row[tid][t] < 0) s.row[tid][t] = (short)~any;
   }
   __syncthreads();
 }
 
 // ---------------------------------------------------------------- item stream
 
+__device__ __forceinline__ uint2 lds_u64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// Scales of four consecutive items (512 k) of one row, as loaded: the 16-byte
+// blocks that hold them.  Rows are K/32 bytes (MXFP4) or K/16 (NF4) apart and
+// aligned to nothing, 4 bytes.  One row per lane: every load touches 32 lines,
+// so they are as wide as they can be (4-byte loads kept the L1 busy for 160
+// cycles per item).
 template <int FMT>
-struct Item {
-  uint32_t w[8];                   // 64 codes: MXFP4 16 bytes of row g, of row g+8; NF4 per row 8 bytes of each block
-  uint32_t s[FMT == 0 ? 4 : 2];    // MXFP4: scale byte per row; NF4: absmax [row][block]
+struct ScaleGroup {
+  uint4 q[FMT == 0 ? 3 : 2];
+  uint32_t off;  // the first scale's byte in q
 };
 
-// A tile's row g of this lane and its scales; the second row lies `hi` rows further.
-struct Rows {
-  const uint8_t* w;
-  const uint8_t* s;
-};
-
+// row: the row's first scale; bytes: of the row; group: 512-k group.  Blocks without a byte of the group are not read.
 template <int FMT>
-__device__ __forceinline__ void load_item(Item<FMT>& it, const Rows& r, size_t w_hi, size_t s_hi, int d, int K, int t) {
-  if (FMT == 1) {
-    const bool ok = d * kDK + 32 * t < K;
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    it.s[0] = it.s[1] = 0u;
-    if (ok) {
-      const uint8_t* w = r.w + (size_t)d * (kDK / 2) + 16 * t;
-      const uint8_t* s = r.s + 4 * d + t;
-      a = ldg_nc_u128(w);
-      b = ldg_nc_u128(w + w_hi);
-      it.s[0] = __ldg(s);
-      it.s[1] = __ldg(s + s_hi);
-    }
-    it.w[0] = a.x, it.w[1] = a.y, it.w[2] = a.z, it.w[3] = a.w;
-    it.w[4] = b.x, it.w[5] = b.y, it.w[6] = b.z, it.w[7] = b.w;
-  } else {
+__device__ __forceinline__ void load_scales(ScaleGroup<FMT>& s, const uint8_t* row, int bytes, int group) {
+  constexpr int kBytes = FMT == 0 ? 32 : 16;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(row) + (size_t)group * kBytes;
+  const uintptr_t down = a & ~(uintptr_t)15;
+  s.off = (uint32_t)(a & 15);
+  const int need = (int)s.off + min(bytes - group * kBytes, kBytes);
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-      const bool ok = d * kDK + 64 * blk < K;
-      uint2 a = make_uint2(0u, 0u), b = a;
-      it.s[blk] = it.s[2 + blk] = 0u;
-      if (ok) {
-        const uint8_t* w = r.w + (size_t)d * (kDK / 2) + 32 * blk + 8 * t;
-        const uint8_t* s = r.s + (size_t)(2 * d + blk) * 4;
-        a = ldg_nc_u64(w);
-        b = ldg_nc_u64(w + w_hi);
-        it.s[blk] = __ldg(reinterpret_cast<const unsigned*>(s));
-        it.s[2 + blk] = __ldg(reinterpret_cast<const unsigned*>(s + s_hi));
-      }
-      it.w[2 * blk] = a.x, it.w[2 * blk + 1] = a.y;
-      it.w[4 + 2 * blk] = b.x, it.w[5 + 2 * blk] = b.y;
+  for (int i = 0; i < (FMT == 0 ? 3 : 2); ++i)
+    s.q[i] = 16 * i < need ? ldg_u128(reinterpret_cast<const void*>(down + 16 * i)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// The group as fp32 in the warp's scratch (this lane's row).  left: scales from the group on (a scale past K is
+// written as 0 or 2^-127: its codes and activations are zero).
+template <int FMT>
+__device__ __forceinline__ void scales_to_scratch(const ScaleGroup<FMT>& s, int left, uint32_t scratch, int lane) {
+  constexpr int kWords = FMT == 0 ? 8 : 5;
+  uint32_t in[FMT == 0 ? 12 : 8], w[kWords];
+#pragma unroll
+  for (int i = 0; i < (FMT == 0 ? 3 : 2); ++i)
+    in[4 * i] = s.q[i].x, in[4 * i + 1] = s.q[i].y, in[4 * i + 2] = s.q[i].z, in[4 * i + 3] = s.q[i].w;
+  const uint32_t o = s.off >> 2;
+  const bool shifted = __any_sync(0xffffffffu, s.off != 0u);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    w[i] = in[i];
+    if (shifted) w[i] = o == 0u ? in[i] : o == 1u ? in[i + 1] : o == 2u ? in[i + 2] : in[i + 3];
+  }
+  if (FMT == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(scratch + kScratchItem * j + scratch_row<FMT>(lane)),
+                   "r"(2 * j < left ? w[2 * j] : 0u), "r"(2 * j + 1 < left ? w[(2 * j + 1) % kWords] : 0u)
+                   : "memory");
+  } else {
+    uint32_t v[4], nan = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = shifted ? __funnelshift_r(w[j % kWords], w[(j + 1) % kWords], 8u * (s.off & 3u)) : w[j % kWords];
+      nan |= (~v[j] - 0x01010101u) & v[j];
+    }
+    if (left < 16)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] &= left <= 4 * j ? 0u : left >= 4 * j + 4 ? 0xFFFFFFFFu : (1u << (8 * (left - 4 * j))) - 1u;
+    const bool any_nan = (nan & 0x80808080u) != 0u;  // a byte may be 255
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // 2^(e - 127): the exponent field, the subnormal 2^-127 for 0, NaN for 255
+      uint32_t f[4] = {(v[j] << 23) & 0x7F800000u, (v[j] << 15) & 0x7F800000u, (v[j] << 7) & 0x7F800000u,
+                       (v[j] >> 1) & 0x7F800000u};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = max(f[i], 0x00400000u);
+      if (any_nan)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (f[i] == 0x7F800000u) f[i] = 0x7FC00000u;
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(scratch + kScratchItem * j + scratch_row<FMT>(lane)),
+                   "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
+                   : "memory");
     }
   }
 }
 
-// acc += the item's 16 x 128 weights times the lane's activations (chunk c = two MMAs).
-template <int FMT>
-__device__ __forceinline__ void multiply(float (&acc)[4], const Item<FMT>& it, const uint4 (&x)[4], uint32_t lanesel) {
-  const uint32_t xp[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
-                           x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
-  if (FMT == 1) {
-    const uint32_t s0 = e8m0_to_bf16x2(it.s[0]), s1 = e8m0_to_bf16x2(it.s[1]);
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// acc += scale of the row * d; TINY: d back in true units (of its column) first.
+template <bool TINY>
+__device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&d)[4], float sa, float sb,
+                                           const float (&unit)[2]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {  // bytes 2j, 2j+1 of both rows
-      const uint32_t b = 2u * (uint32_t)(j & 1);
-      const uint32_t a0 = bf16x2_mul(lookup(it.w[j >> 1], lanesel, b), s0);
-      const uint32_t a1 = bf16x2_mul(lookup(it.w[4 + (j >> 1)], lanesel, b), s1);
-      const uint32_t a2 = bf16x2_mul(lookup(it.w[j >> 1], lanesel, b + 1u), s0);
-      const uint32_t a3 = bf16x2_mul(lookup(it.w[4 + (j >> 1)], lanesel, b + 1u), s1);
-      mma_bf16_16816(acc, a0, a1, a2, a3, xp[2 * j], xp[2 * j + 1]);
+  for (int i = 0; i < 4; ++i) acc[i] = fmaf(i < 2 ? sa : sb, TINY ? d[i] * unit[i & 1] : d[i], acc[i]);
+}
+
+// acc[tile] += the item's weights (shared memory) times the lane's activations: chunk c at x + c * x_step.
+// Tile k holds item rows r0 + 8 STEP_T k (its first 8) and 8 STEP_H further.
+template <int FMT, bool TINY, int STEP_T, int STEP_H>
+__device__ __forceinline__ void multiply(float (&acc)[2][4], uint32_t item, uint32_t scratch, uint32_t x,
+                                         uint32_t x_step, const float (&unit)[2], int r0, int t, uint32_t lanesel) {
+  const uint32_t key = (uint32_t)(r0 >> 1) & 3u;  // the box's 64-byte swizzle: 16-byte chunk ^= (row / 2) % 4
+  if (FMT == 1) {
+    const uint32_t at = item + 64 * r0 + 4 * t + (key << 4);
+    scratch += 16 * r0;
+    uint4 v[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) v[b] = lds_u128(x + b * x_step);
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      const int ra = 8 * STEP_T * tile, rb = ra + 8 * STEP_H;
+      const uint4 qa = lds_u128(scratch + scratch_row<FMT>(ra)), qb = lds_u128(scratch + scratch_row<FMT>(rb));
+      const float sa[4] = {__uint_as_float(qa.x), __uint_as_float(qa.y), __uint_as_float(qa.z), __uint_as_float(qa.w)};
+      const float sb[4] = {__uint_as_float(qb.x), __uint_as_float(qb.y), __uint_as_float(qb.z), __uint_as_float(qb.w)};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {  // one 32-block: this lane's 8 codes of each row
+        const uint32_t q = at ^ ((uint32_t)b << 4);
+        uint32_t lo[4], hi[4];
+        e2m1_to_f16(lds_u32(q + 64 * ra), lo);
+        e2m1_to_f16(lds_u32(q + 64 * rb), hi);
+        float d[4];
+        mma_new(d, lo[0], hi[0], lo[1], hi[1], v[b].x, v[b].y);
+        mma_add(d, lo[2], hi[2], lo[3], hi[3], v[b].z, v[b].w);
+        add_scaled<TINY>(acc[tile], d, sa[b], sb[b], unit);
+      }
     }
   } else {
+    const uint32_t at = item + 64 * r0 + 8 * (t & 1);
+    scratch += 8 * r0;
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < 2; ++b) {  // one 64-block: 16 codes of each row
+      const uint32_t q = at + (((uint32_t)(2 * b + (t >> 1)) ^ key) << 4);
+      const uint4 v0 = lds_u128(x + 2 * b * x_step), v1 = lds_u128(x + (2 * b + 1) * x_step);
 #pragma unroll
-      for (int j = 4 * blk; j < 4 * blk + 4; ++j) {
-        const uint32_t b = 2u * (uint32_t)(j & 1);
-        mma_bf16_16816(d, lookup(it.w[j >> 1], lanesel, b), lookup(it.w[4 + (j >> 1)], lanesel, b),
-                       lookup(it.w[j >> 1], lanesel, b + 1u), lookup(it.w[4 + (j >> 1)], lanesel, b + 1u), xp[2 * j],
-                       xp[2 * j + 1]);
+      for (int tile = 0; tile < 2; ++tile) {
+        const int ra = 8 * STEP_T * tile, rb = ra + 8 * STEP_H;
+        const uint2 va = lds_u64(q + 64 * ra), vb = lds_u64(q + 64 * rb);
+        const float sa = lds_f32(scratch + scratch_row<FMT>(ra) + 4 * b), sb = lds_f32(scratch + scratch_row<FMT>(rb) + 4 * b);
+        float d[4];
+        mma_new(d, lookup(va.x, lanesel, 0), lookup(vb.x, lanesel, 0), lookup(va.x, lanesel, 1),
+                lookup(vb.x, lanesel, 1), v0.x, v0.y);
+        mma_add(d, lookup(va.x, lanesel, 2), lookup(vb.x, lanesel, 2), lookup(va.x, lanesel, 3),
+                lookup(vb.x, lanesel, 3), v0.z, v0.w);
+        mma_add(d, lookup(va.y, lanesel, 0), lookup(vb.y, lanesel, 0), lookup(va.y, lanesel, 1),
+                lookup(vb.y, lanesel, 1), v1.x, v1.y);
+        mma_add(d, lookup(va.y, lanesel, 2), lookup(vb.y, lanesel, 2), lookup(va.y, lanesel, 3),
+                lookup(vb.y, lanesel, 3), v1.z, v1.w);
+        add_scaled<TINY>(acc[tile], d, sa, sb, unit);
       }
-      const float s0 = __uint_as_float(it.s[blk]), s1 = __uint_as_float(it.s[2 + blk]);
-      acc[0] = fmaf(s0, d[0], acc[0]);
-      acc[1] = fmaf(s0, d[1], acc[1]);
-      acc[2] = fmaf(s1, d[2], acc[2]);
-      acc[3] = fmaf(s1, d[3], acc[3]);
     }
   }
 }
 
-// One phase's view of its item sequence: unit u = items [u * per, (u + 1) * per).
-template <int FMT, int PHASE>
-struct Stream {
-  const MoeDecodeArgs& p;
-  const Tables& s;
-  const uint4* xs;  // shared x in fragment order (phase 2)
-  int g, t, K, nd, per, cols;  // nd: items of one expert; cols: units of an expert (phase 2)
-  size_t w_hi, s_hi, wrow, srow;
-
-  __device__ __forceinline__ Stream(const MoeDecodeArgs& p_, const Tables& s_, const uint4* xs_, int lane)
-      : p(p_), s(s_), xs(xs_), g(lane >> 2), t(lane & 3) {
-    K = PHASE == 2 ? p.H : p.I;
-    nd = (K + kDK - 1) / kDK;
-    cols = p.I / 8;
-    per = PHASE == 2 ? nd : nd * s.nhit;
-    wrow = (size_t)(K / 2);
-    srow = FMT == 0 ? (size_t)(K / 64) * 4 : (size_t)(K / 32);
-    const size_t hi = PHASE == 2 ? (size_t)p.I : 8;
-    w_hi = hi * wrow;
-    s_hi = hi * srow;
-  }
-  __device__ __forceinline__ Rows rows(int unit, int ei) const {
-    // phase 2: unit = (hit expert, 8 columns); phase 3: unit = 16 output rows, ei = hit expert
-    const int e = PHASE == 2 ? s.expert[unit / cols] : s.expert[ei];
-    const size_t n = PHASE == 2 ? (size_t)e * (2 * (size_t)p.I) + 8 * (size_t)(unit % cols) + g
-                                : (size_t)e * (size_t)p.H + 16 * (size_t)unit + g;
-    const uint8_t* w = PHASE == 2 ? p.w1 : p.w2;
-    const void* sc = PHASE == 2 ? p.s1 : p.s2;
-    return Rows{w + n * wrow, static_cast<const uint8_t*>(sc) + n * srow};
-  }
-  __device__ __forceinline__ void load_x(uint4 (&x)[4], int ei, int d) const {
-    if (PHASE == 2) {
-      if (g < p.T) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = xs[(size_t)(d * 4 + c) * (4 * p.T) + 4 * g + t];
-      }
-    } else {
-      const int r = g < p.T ? s.row[ei][g] : -1;
-      const uint4* h = reinterpret_cast<const uint4*>(p.hbuf) + ((size_t)max(r, 0) * nd + d) * 16 + t;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool ok = r >= 0 && d * kDK + chunk_k<FMT>(t, c) < K;
-        x[c] = ok ? __ldcg(h + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
+// `total` things divided evenly over `parts`: part c holds [begin(c), begin(c + 1)).
+struct Share {
+  int base, extra;  // the first `extra` parts hold one more
+  __device__ __forceinline__ Share(int total, unsigned parts) : base(total / (int)parts), extra(total % (int)parts) {}
+  __device__ __forceinline__ int begin(int c) const { return c * base + min(c, extra); }
+  __device__ __forceinline__ int owner(int i) const {
+    const int big = extra * (base + 1);
+    return i < big ? i / (base + 1) : extra + (i - big) / base;
   }
 };
 
@@ -412,260 +540,544 @@ struct Stream {
 struct Cursor {
   int unit, ei, d;
 };
-template <int PHASE>
-__device__ __forceinline__ Cursor cursor_at(int item, int per, int nd) {
-  Cursor c;
-  c.unit = item / per;
-  const int q = item - c.unit * per;
-  c.ei = PHASE == 2 ? 0 : q / nd;
-  c.d = PHASE == 2 ? q : q - c.ei * nd;
-  return c;
-}
-// Advances by one item; true if the tile's rows change.
-template <int PHASE>
-__device__ __forceinline__ bool advance(Cursor& c, int nd, int nhit) {
-  if (++c.d < nd) return false;
-  c.d = 0;
-  if (PHASE == 2) {
-    ++c.unit;
-  } else if (++c.ei == nhit) {
-    c.ei = 0;
-    ++c.unit;
+
+// One phase's view of its item sequence: unit u = items [u * per, (u + 1) * per).
+template <int FMT, int PHASE>
+struct Stream {
+  const MoeDecodeArgs& p;
+  const Route& s;
+  const Work& wk;
+  const CUtensorMap* map;
+  int g, t, lane, nd, per, cols, nhit;  // nd: items of one expert; cols: units of an expert (phase 2)
+  int ns, srow;                         // scales and scale bytes of a row
+
+  __device__ __forceinline__ Stream(const MoeDecodeArgs& p_, const Route& s_, const Work& wk_, const CUtensorMap* map_,
+                                    int lane_)
+      : p(p_), s(s_), wk(wk_), map(map_), g(lane_ >> 2), t(lane_ & 3), lane(lane_), nhit(wk_.nhit) {
+    const int K = PHASE == 2 ? p.H : p.I;
+    nd = (K + kDK - 1) / kDK;
+    cols = p.I / 16;
+    per = PHASE == 2 ? nd : nd * nhit;
+    ns = FMT == 0 ? K / 64 : K / 32;
+    srow = ns * (FMT == 0 ? 4 : 1);
   }
-  return true;
-}
+  __device__ __forceinline__ Cursor at(int item) const {
+    Cursor c;
+    c.unit = item / per;
+    const int q = item - c.unit * per;
+    c.ei = PHASE == 2 ? c.unit / cols : q / nd;
+    c.d = PHASE == 2 ? q : q - c.ei * nd;
+    return c;
+  }
+  // Advances by one item; true if the tile's rows change.
+  __device__ __forceinline__ bool advance(Cursor& c) const {
+    if (++c.d < nd) return false;
+    c.d = 0;
+    if (PHASE == 2) {
+      c.ei = ++c.unit / cols;
+    } else if (++c.ei == nhit) {
+      c.ei = 0;
+      ++c.unit;
+    }
+    return true;
+  }
+  // One box: phase 2: 16 gate rows, then the 16 up rows; phase 3: 32 rows.
+  __device__ __forceinline__ void load_box(void* dst, uint64_t* bar, const Cursor& c) const {
+    mbar_arrive_expect_tx(bar, kItemBytes);
+    const int e = s.expert[c.ei];
+    if (PHASE == 2)
+      tma_load_4d(dst, map, bar, (kDK / 2) * c.d, 16 * (c.unit - c.ei * cols), 0, e);
+    else
+      tma_load_3d(dst, map, bar, (kDK / 2) * c.d, 32 * c.unit, e);
+  }
+  // First scale of item row `lane`.
+  __device__ __forceinline__ const uint8_t* scale_row(const Cursor& c) const {
+    const size_t e = (size_t)s.expert[c.ei];
+    const size_t n = PHASE == 2 ? e * (2 * (size_t)p.I) + 16 * (size_t)(c.unit - c.ei * cols) + (lane & 15) +
+                                      (lane < 16 ? 0 : (size_t)p.I)
+                                : e * (size_t)p.H + 32 * (size_t)c.unit + lane;
+    return static_cast<const uint8_t*>(PHASE == 2 ? p.s1 : p.s2) + n * (size_t)srow;
+  }
+  // Phase 3: the pair whose h this lane multiplies (a column without the token takes another: its sums are dropped).
+  __device__ __forceinline__ int pair(int ei) const {
+    const int r = s.row[ei][g];
+    return r < 0 ? ~r : r;
+  }
+  __device__ __forceinline__ void load_h(float4 (&h)[8], const Cursor& c) const {
+    const float4* q = reinterpret_cast<const float4*>(p.hbuf) + (((size_t)pair(c.ei) * nd + c.d) * 16 + t) * 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __ldcg(q + 8 * (i >> 1) + (i & 1));
+  }
+  __device__ __forceinline__ void store_h(uint32_t slot, const float4 (&h)[8], const Cursor& c) const {
+    const float sc = wk.hscale[pair(c.ei)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = h[2 * i], b = h[2 * i + 1];
+      __half2 v[4] = {__floats2half2_rn(a.x * sc, a.y * sc), __floats2half2_rn(a.z * sc, a.w * sc),
+                      __floats2half2_rn(b.x * sc, b.y * sc), __floats2half2_rn(b.z * sc, b.w * sc)};
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(slot + 512 * i), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                   "r"(u[3])
+                   : "memory");
+    }
+  }
+  // 1 / the scale of column q (0, 1) of this lane; 0 for a phase 3 column whose token did not choose expert ei.
+  __device__ __forceinline__ float unit_of(int ei, int q) const {
+    const int col = 2 * t + q;
+    if (PHASE == 2) return scale_down(wk.xmax[col]);
+    const int r = s.row[ei][col];
+    return r < 0 ? 0.f : 1.0f / wk.hscale[r];  // a power of two: exact
+  }
+};
+
+// A warp's ring of boxes: slot and phase of the next box to issue and to read.
+struct Ring {
+  uint32_t base;   // shared address
+  uint8_t* ptr;
+  uint64_t* full;
+  int stages;
+  int put, get;
+  uint32_t parity;
+  __device__ __forceinline__ void pushed() { put = put + 1 == stages ? 0 : put + 1; }
+  __device__ __forceinline__ void popped() {
+    if (++get == stages) {
+      get = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // Streams the CTA's items [a, b): `ready` runs once the first loads are in
 // flight (a barrier may hide behind them), `emit(unit, acc, whole)` is called
 // by one full warp per unit of the range, whole = all of its items were here.
-// Returns false if `ready` did.
-template <int FMT, int PHASE, class Ready, class Emit>
-__device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Tables& s, int a, int b, uint32_t lanesel,
-                                           int warp, int lane, Ready ready, Emit emit) {
-  const int n = b - a, per = st.per, nd = st.nd, nhit = s.nhit;
-  auto split = [&](int w) { return a + (int)((long long)n * w / kWarps); };
-  const int lo = split(warp), hi = split(warp + 1);
-  Item<FMT> it[kStages];
-  Cursor ld = cursor_at<PHASE>(lo, per, nd);
-  Rows rows{nullptr, nullptr};
-  int next = lo;
-  if (lo < hi) rows = st.rows(ld.unit, ld.ei);
-  auto fetch = [&](Item<FMT>& dst) {
-    if (next < hi) {
-      load_item<FMT>(dst, rows, st.w_hi, st.s_hi, ld.d, st.K, st.t);
-      ++next;
-      if (advance<PHASE>(ld, nd, nhit) && next < hi) rows = st.rows(ld.unit, ld.ei);
+// x: phase 2 this lane's x in shared memory (items 4 * x_step apart), phase 3
+// its slot for h.  A wait that gives up flags the timeout; the stream then runs
+// to its end on whatever the ring holds.
+template <int FMT, int PHASE, bool TINY, class Emit>
+__device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Work& wk, unsigned* err, int a,
+                                           int b, int lo, int hi, int next, Cursor ld, uint32_t scratch, uint32_t x,
+                                           uint32_t x_step, uint32_t lanesel, uint8_t* rings, int warp, float4 (&h)[8],
+                                           Emit emit) {
+  const int n = b - a, per = st.per, lane = st.lane;
+  auto split = [&](int w) { return a + n * w / kWarps; };
+  // NF4 reads 8 bytes per lane: this order of the 8 rows keeps each half of the warp on 32 banks
+  const int r0 = FMT == 0 ? (st.g & 1) | ((st.g & 2) << 1) | ((st.g & 4) >> 1) : st.g;
+  Cursor cur = st.at(lo);
+  ScaleGroup<FMT> sc;
+  // the group after the one at c, if it belongs to this warp (item: index of c)
+  auto load_next_group = [&](const Cursor& c, int item) {
+    const int skip = min(4 - (c.d & 3), st.nd - c.d);
+    if (item + skip >= hi) return;
+    Cursor q = c;
+    if (q.d + skip < st.nd) {
+      q.d += skip;
+    } else {
+      q.d = st.nd - 1;
+      st.advance(q);
     }
+    load_scales<FMT>(sc, st.scale_row(q), st.srow, q.d >> 2);
   };
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) fetch(it[i]);
-  if (!ready()) return false;
-
-  Cursor cur = cursor_at<PHASE>(lo, per, nd);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  float one[4] = {0.f, 0.f, 0.f, 0.f};  // phase 3: the current expert's part
-  uint4 x[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) x[c] = make_uint4(0u, 0u, 0u, 0u);
+  if (lo < hi) {
+    load_scales<FMT>(sc, st.scale_row(cur), st.srow, cur.d >> 2);
+    if (PHASE == 3) st.store_h(x, h, cur);
+  }
+  float acc[2][4] = {};
+  float one[2][4] = {};   // phase 3: the current expert's part
+  float head[2][4] = {};  // a unit begun by an earlier warp
+  float unit2[2] = {1.0f, 1.0f};
+  if (PHASE == 2) unit2[0] = st.unit_of(0, 0), unit2[1] = st.unit_of(0, 1);
   bool tail = false;  // a unit begun by this warp and not finished by it
-  for (int i = lo; i < hi; i += kStages) {
+  for (int item = lo; item < hi; ++item) {
+    if (item == lo || (cur.d & 3) == 0) {
+      scales_to_scratch<FMT>(sc, st.ns - (cur.d >> 2) * (FMT == 0 ? 8 : 16), scratch, lane);
+      load_next_group(cur, item);
+    }
+    const int unit = cur.unit, ei = cur.ei;
+    const uint32_t sa = scratch + (cur.d & 3) * kScratchItem;
+    const uint32_t xa = PHASE == 2 ? x + 4 * x_step * cur.d : x;
+    const bool turn = st.advance(cur), more = item + 1 < hi;
+    if (PHASE == 3 && more) st.load_h(h, cur);
+    if (PHASE == 3 && TINY) unit2[0] = st.unit_of(ei, 0), unit2[1] = st.unit_of(ei, 1);
+    mbar_wait(ring.full + ring.get, ring.parity, err, &wk.abort);
+    __syncwarp();
+    multiply<FMT, TINY, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(PHASE == 3 ? one : acc,
+                                                                ring.base + ring.get * kItemBytes, sa, xa, x_step,
+                                                                unit2, r0, st.t, lanesel);
+    ring.popped();
+    __syncwarp();  // every lane has read the box and the scratch
+    if (next < hi) {
+      if (lane == 0) st.load_box(ring.ptr + ring.put * kItemBytes, ring.full + ring.put, ld);
+      ring.pushed();
+      ++next;
+      st.advance(ld);
+    }
+    if (PHASE == 3 && more) st.store_h(x, h, cur);
+    if (!turn && more) continue;
+    if (PHASE == 3) {
+      // columns of tokens that did not choose the expert are dropped, not
+      // added as zeros: 0 times a NaN or infinite weight is NaN
 #pragma unroll
-    for (int j = 0; j < kStages; ++j) {
-      const int item = i + j;
-      if (item < hi) {
-        st.load_x(x, cur.ei, cur.d);
-        multiply<FMT>(PHASE == 3 ? one : acc, it[j], x, lanesel);
-        fetch(it[j]);
-        const int unit = cur.unit, ei = cur.ei;
-        const bool turn = advance<PHASE>(cur, nd, nhit);
-        if (PHASE == 3 && (turn || item + 1 == hi)) {
-          // columns of tokens that did not choose the expert are dropped, not
-          // added as zeros: 0 times a NaN or infinite weight is NaN
+      for (int q = 0; q < 2; ++q) {
+        const float u = st.unit_of(ei, q);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[q] += s.row[ei][2 * st.t + (q & 1)] >= 0 ? one[q] : 0.f;
-            one[q] = 0.f;
-          }
-        }
-        if (cur.unit != unit || item + 1 == hi) {
-          const int first = max(unit * per, a), last = min((unit + 1) * per, b);  // the unit's items in this CTA
-          if (lo <= first && last <= hi) {
-            emit(unit, acc, last - first == per);
-          } else {
-            tail = lo <= first;
-            *reinterpret_cast<float4*>(&s.part[warp][tail ? 1 : 0][lane][0]) =
-                make_float4(acc[0], acc[1], acc[2], acc[3]);
-          }
-          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        for (int k = 0; k < 2; ++k) {
+          acc[k][q] += u != 0.f ? (TINY ? one[k][q] : one[k][q] * u) : 0.f;
+          acc[k][q + 2] += u != 0.f ? (TINY ? one[k][q + 2] : one[k][q + 2] * u) : 0.f;
+          one[k][q] = one[k][q + 2] = 0.f;
         }
       }
     }
+    if (more && cur.unit == unit) continue;
+    const int first = max(unit * per, a), last = min((unit + 1) * per, b);  // the unit's items in this CTA
+    if (lo <= first && last <= hi) {
+      emit(unit, acc, last - first == per, r0, unit2);
+    } else if (lo <= first) {
+      tail = true;  // stays in acc: this was the last item
+      break;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) head[k][i] = acc[k][i];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
   }
+  // the ring is idle: its first KB takes the head part
+  auto part = [&](int w) { return reinterpret_cast<float4*>(rings + (size_t)w * ring.stages * kItemBytes) + lane; };
+#pragma unroll
+  for (int k = 0; k < 2; ++k) part(warp)[32 * k] = make_float4(head[k][0], head[k][1], head[k][2], head[k][3]);
   __syncthreads();
-  if (tail) {  // the unit of this warp's last item: add the parts of the warps after it
+  if (tail) {  // add the parts of the warps after this one
     const int unit = (hi - 1) / per;
     const int first = max(unit * per, a), last = min((unit + 1) * per, b);
-    float4 v = *reinterpret_cast<const float4*>(&s.part[warp][1][lane][0]);
     for (int w = warp + 1; w < kWarps && split(w) < last; ++w) {
       if (split(w) == split(w + 1)) continue;
-      const float4 o = *reinterpret_cast<const float4*>(&s.part[w][0][lane][0]);
-      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 v = part(w)[32 * k];
+        acc[k][0] += v.x, acc[k][1] += v.y, acc[k][2] += v.z, acc[k][3] += v.w;
+      }
     }
-    float sum[4] = {v.x, v.y, v.z, v.w};
-    emit(unit, sum, last - first == per);
+    emit(unit, acc, last - first == per, r0, unit2);
   }
-  return true;
+}
+
+// A warp's items of the CTA's [a, b), and the first boxes on their way.
+template <int FMT, int PHASE>
+__device__ __forceinline__ void start_stream(const Stream<FMT, PHASE>& st, Ring& ring, int a, int b, int warp, int* lo,
+                                             int* hi, int* next, Cursor* ld) {
+  const int n = b - a;
+  *lo = a + n * warp / kWarps;
+  *hi = a + n * (warp + 1) / kWarps;
+  *ld = st.at(*lo);
+  *next = *lo;
+  // earlier generic accesses to the ring (partial sums) before the boxes
+  fence_proxy_async_smem();
+  __syncwarp();
+  for (int i = 0; i < ring.stages && *next < *hi; ++i) {
+    if (st.lane == 0) st.load_box(ring.ptr + ring.put * kItemBytes, ring.full + ring.put, *ld);
+    ring.pushed();
+    ++*next;
+    st.advance(*ld);
+  }
+}
+
+// x as fp16 scaled per token, in fragment order, zero past H.  All threads;
+// a token belongs to 16 / TP warps (TP: T up to a power of two).
+template <int FMT>
+__device__ __forceinline__ void stage_x(const MoeDecodeArgs& p, Work& s, uint4* xs, int tid) {
+  const int nd = (p.H + kDK - 1) / kDK, H8 = p.H / 8;
+  const int wpt = p.T == 1 ? 16 : p.T == 2 ? 8 : p.T <= 4 ? 4 : 2;
+  const int tok = (tid >> 5) / wpt, first = ((tid >> 5) % wpt) * 32 + (tid & 31), step = wpt * 32;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x) + (size_t)tok * H8;
+  if (tok < p.T) {
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int i = first; i < H8; i += step) {
+      const uint4 v = __ldg(x + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
+        m = max(m, max(a >= 0x7F80u ? 0u : a, b >= 0x7F80u ? 0u : b));
+      }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) atomicMax(&s.xmax[tok], m << 16);
+  }
+  __syncthreads();
+  if (tok >= p.T) return;
+  const float sc = scale_up(s.xmax[tok]);
+#pragma unroll 8
+  for (int i = first; i < nd * 16; i += step) {
+    uint4 v = i < H8 ? __ldg(x + i) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * sc, __uint_as_float(w[j] & 0xFFFF0000u) * sc);
+      w[j] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    const int at = chunk_of<FMT>(8 * (i & 15));  // 4 * c + t
+    xs[((i >> 4) * 4 + (at >> 2)) * 4 * p.T + 4 * tok + (at & 3)] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(MoeDecodeArgs p, uint32_t table_at, uint32_t smem_end) {
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_decode_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
+                      const MoeDecodeArgs p, const Plan plan) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t base = smem_u32(smem_raw);
-  const uint32_t x_bytes = (uint32_t)((p.H + kDK - 1) / kDK) * 256u * (uint32_t)p.T;
-  // guards against a shared window placed otherwise than the host assumed
-  if (base + x_bytes > table_at || table_at + (uint32_t)kLut256Bytes + sizeof(Tables) > base + smem_end) {
+  if (smem_u32(smem_raw) != kWindow) {  // the plan's alignments assume it
     if (tid == 0) atomicOr(p.err, GNF4_DEVERR_INTERNAL);
     return;
   }
   uint4* xs = reinterpret_cast<uint4*>(smem_raw);
-  Tables& s = *reinterpret_cast<Tables*>(smem_raw + (table_at - base) + (uint32_t)kLut256Bytes);
-  build_table<FMT>(reinterpret_cast<uint32_t*>(smem_raw + (table_at - base)), tid);
-  const uint32_t lanesel = (uint32_t)lane * 4u | (table_at & 0x00FF0000u);
-  {  // x in fragment order, zero past H
-    const int nd = (p.H + kDK - 1) / kDK;
-    for (int i = tid; i < nd * 16 * p.T; i += kThreads) {
-      const int l = i % (4 * p.T), c = (i / (4 * p.T)) & 3, d = i / (16 * p.T);
-      const int k = d * kDK + chunk_k<FMT>(l & 3, c);
-      xs[i] = k < p.H ? ldg_u128(p.x + (size_t)(l >> 2) * p.H + k) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-  if (tid < kMaxExperts / 32) s.hit[tid] = 0u;
-  if (p.router_w != nullptr) {
-    router_product(p, s, tid);
-    if (!grid_barrier(&p.sync[0], p.err, &s.ok)) return;
-  }
-  __syncthreads();
-  if (warp < p.T) select_topk(p, s, warp, lane);
-  __syncthreads();
-  list_hits(p, s, tid);
+  Route& rt = *reinterpret_cast<Route*>(smem_raw + plan.route);
+  Work& wk = *reinterpret_cast<Work*>(smem_raw + plan.work);
+  const uint32_t scratch = kWindow + plan.scratch + (uint32_t)(warp * kScratchStride);
+  uint8_t* rings = smem_raw + plan.ring;
+  Ring ring{};
+  ring.ptr = rings + (size_t)warp * plan.stages * kItemBytes;
+  ring.base = smem_u32(ring.ptr);
+  ring.full = wk.full[warp];
+  ring.stages = plan.stages;
 
-  const float inv_gain = FMT == 0 ? 1.0f / kNf4Gain : 1.0f;
-  {  // gate_up + SwiGLU; h times its router weight goes to the workspace in fragment order
-    const Stream<FMT, 2> st(p, s, xs, lane);
-    const long long units = (long long)s.nhit * st.cols;
-    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
-    const int nd2 = (p.I + kDK - 1) / kDK;
-    run_stream<FMT, 2>(
-        st, s, u0 * st.per, u1 * st.per, lanesel, warp, lane, [] { return true; },
-        [&](int unit, const float(&acc)[4], bool) {
-          const int ei = unit / st.cols, col = 8 * (unit % st.cols);
-          const int d = col / kDK, q = col % kDK;  // the 8 columns are one chunk
-          const int tt = FMT == 0 ? (q & 63) >> 4 : q >> 5;
-          const int c = FMT == 0 ? 2 * (q >> 6) + ((q >> 3) & 1) : (q >> 3) & 3;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tok = 2 * t + i;
-            const int r = tok < p.T ? s.row[ei][tok] : -1;
-            if (r < 0) continue;
-            const float v = silu_mul(acc[i] * inv_gain, acc[2 + i] * inv_gain) * s.wt[ei][tok];
-            p.hbuf[(((size_t)r * nd2 + d) * 16 + 4 * c + tt) * 8 + g] = __float2bfloat16_rn(v);
-          }
-        });
+  if (tid < kMaxExperts / 32) rt.hit[tid] = 0u;
+  if (tid < kMaxT) wk.xmax[tid] = 0u;
+  if (tid == 0) {
+    wk.abort = 0;
+    wk.tiny = 0;
+    prefetch_tmap(&map1);
+    prefetch_tmap(&map2);
   }
-  {  // down + combine
-    const Stream<FMT, 3> st(p, s, xs, lane);
-    const long long items = (long long)(p.H / 16) * st.per;
-    const long long G = items < gridDim.x ? items : gridDim.x;
-    const bool mine = (long long)blockIdx.x < G;
-    const int a = mine ? (int)(items * blockIdx.x / G) : 0, b = mine ? (int)(items * (blockIdx.x + 1) / G) : 0;
-    auto store = [&](int unit, const float(&acc)[4]) {
+  if (lane < plan.stages) mbar_init(ring.full + lane, 1);
+  fence_mbar_init();
+  // the table and x are laid out while the router's first weights arrive
+  const RouterPart part(p, tid);
+  __syncthreads();
+  if (FMT == 0) build_table(reinterpret_cast<uint32_t*>(smem_raw + plan.table), tid);
+  stage_x<FMT>(p, wk, xs, tid);
+  if (p.router_w != nullptr) {
+    if (p.T == 1) router_product<1>(p, wk, part, tid);
+    else if (p.T == 2) router_product<2>(p, wk, part, tid);
+    else if (p.T <= 4) router_product<4>(p, wk, part, tid);
+    else router_product<8>(p, wk, part, tid);
+    grid_arrive(&p.sync[0]);
+  }
+  const int nd2 = (p.I + kDK - 1) / kDK;
+  if (p.I % kDK != 0) {  // the last item of every row of h: zero past I
+    const int pad = (nd2 * kDK - p.I) / 8;  // chunks
+    for (int row = blockIdx.x; row < p.T * p.k; row += gridDim.x)
+      for (int i = tid; i < 2 * pad; i += kThreads) {
+        const int c = chunk_of<FMT>(p.I % kDK + 8 * (i >> 1));
+        reinterpret_cast<float4*>(p.hbuf)[(((size_t)row * nd2 + nd2 - 1) * 16 + c) * 2 + (i & 1)] =
+            make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+  }
+  if (p.router_w != nullptr) {
+    if (!grid_wait(&p.sync[0], p.err, &wk.ok)) return;
+  } else {
+    __syncthreads();
+  }
+  if (warp < p.T) {
+    if (p.E <= 64) select_topk<2>(p, rt, warp, lane);
+    else if (p.E <= 128) select_topk<4>(p, rt, warp, lane);
+    else if (p.E <= 384) select_topk<12>(p, rt, warp, lane);
+    else select_topk<kMaxExperts / 32>(p, rt, warp, lane);
+  }
+  __syncthreads();
+  list_hits(p, rt, &wk.nhit, tid);
+  const uint32_t lanesel = (uint32_t)lane * 4u | ((kWindow + plan.table) & 0x00FF0000u);
+  int lo, hi, next;
+  Cursor ld;
+  float4 h[8] = {};  // phase 3: the next item's activations on their way
+
+  {  // gate_up + SwiGLU; h times its router weight goes to the workspace in fragment order
+    const Stream<FMT, 2> st(p, rt, wk, &map1, lane);
+    const Share sh(wk.nhit * st.cols, gridDim.x);
+    const int a = sh.begin(blockIdx.x) * st.per, b = sh.begin(blockIdx.x + 1) * st.per;
+    start_stream<FMT, 2>(st, ring, a, b, warp, &lo, &hi, &next, &ld);
+    bool tiny = false;
+    for (int i = 0; i < p.T; ++i) tiny |= is_tiny(wk.xmax[i]);
+    // columns past T repeat the last token and are never stored
+    const uint32_t x = kWindow + 16u * (4 * min(g, p.T - 1) + t), x_step = 64u * p.T;
+    auto emit = [&](int unit, const float(&acc)[2][4], bool, int r0, const float(&xu)[2]) {
+      const int ei = unit / st.cols;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 2 * t + (i & 1);
-        if (tok < p.T) p.out[(size_t)tok * p.H + 16 * unit + g + 8 * (i >> 1)] = __float2bfloat16_rn(acc[i] * inv_gain);
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 2 * t + i, r = rt.row[ei][tok];
+        const float u = tiny ? 1.0f : xu[i], w = r < 0 ? 0.f : rt.sel_p[r];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = 16 * (unit - ei * st.cols) + 8 * k;  // 8 columns = one chunk
+          const size_t chunk = (size_t)(col / kDK) * 16 + chunk_of<FMT>(col % kDK);
+          if (r < 0) continue;
+          const float v = silu_mul(acc[k][i] * u, acc[k][2 + i] * u) * w;
+          p.hbuf[((size_t)r * nd2 * 16 + chunk) * 8 + r0] = v;
+          const uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
+          top = max(top, m >= 0x7F800000u ? 0u : m);
+        }
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (r >= 0 && g == 0) atomicMax(p.hmax + r, top);
       }
     };
-    const bool ok = run_stream<FMT, 3>(
-        st, s, a, b, lanesel, warp, lane, [&] { return grid_barrier(&p.sync[1], p.err, &s.ok); },
-        [&](int unit, const float(&acc)[4], bool whole) {
-          if (whole) {
-            store(unit, acc);
-            return;
-          }
-          // the CTAs of the unit's first and last item; all between them hold a part
-          const long long q0 = (long long)unit * st.per, q1 = q0 + st.per - 1;
-          const int c0 = (int)(((q0 + 1) * G - 1) / items), c1 = (int)(((q1 + 1) * G - 1) / items);
-          float4* part = reinterpret_cast<float4*>(p.part);
-          part[((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * 32 + lane] =
-              make_float4(acc[0], acc[1], acc[2], acc[3]);
-          __threadfence();
-          __syncwarp();
-          int last = 0;
-          if (lane == 0) {
-            last = atomicAdd(p.unit_count + unit, 1u) == (unsigned)(c1 - c0);
-            if (last) p.unit_count[unit] = 0u;
-            __threadfence();
-          }
-          last = __shfl_sync(0xffffffffu, last, 0);
-          __syncwarp();
-          if (!last) return;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int c = c0; c <= c1; ++c) {
-            const float4 v = __ldcg(part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * 32 + lane);
-            sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
-          }
-          store(unit, sum);
-        });
-    if (!ok) return;
+    if (tiny)
+      run_stream<FMT, 2, true>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, x, x_step, lanesel, rings, warp, h,
+                               emit);
+    else
+      run_stream<FMT, 2, false>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, x, x_step, lanesel, rings, warp, h,
+                                emit);
   }
-  // the last CTA to leave zeroes the barrier words
-  if (tid == 0) {
-    if (atomicAdd(&p.sync[2], 1u) == gridDim.x - 1) {
-      p.sync[0] = p.sync[1] = p.sync[2] = 0u;
+  {  // down + combine
+    const Stream<FMT, 3> st(p, rt, wk, &map2, lane);
+    const Share sh((p.H / 32) * st.per, gridDim.x);
+    const int a = sh.begin(blockIdx.x), b = sh.begin(blockIdx.x + 1);
+    auto store = [&](int unit, const float(&acc)[2][4], int r0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 2 * t + (i & 1);
+          if (tok < p.T) p.out[(size_t)tok * p.H + 32 * unit + 16 * k + r0 + 8 * (i >> 1)] = __float2bfloat16_rn(acc[k][i]);
+        }
+    };
+    auto emit = [&](int unit, const float(&acc)[2][4], bool whole, int r0, const float(&)[2]) {
+      if (whole) {
+        store(unit, acc, r0);
+        return;
+      }
+      // the CTAs of the unit's first and last item; all between them hold a part
+      const int c0 = sh.owner(unit * st.per), c1 = sh.owner((unit + 1) * st.per - 1);
+      float4* part = reinterpret_cast<float4*>(p.part) + lane;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        part[(((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * 2 + k) * 32] =
+            make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) {
+        last = atom_add_acq_rel(p.unit_count + unit, 1u) == (unsigned)(c1 - c0);
+        if (last) p.unit_count[unit] = 0u;
+      }
+      last = __shfl_sync(0xffffffffu, last, 0);
+      __syncwarp();
+      if (!last) return;
+      float sum[2][4] = {};
+      for (int c = c0; c <= c1; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 v = __ldcg(part + (((size_t)c * 2 + (c == c0 ? 1 : 0)) * 2 + k) * 32);
+          sum[k][0] += v.x, sum[k][1] += v.y, sum[k][2] += v.z, sum[k][3] += v.w;
+        }
+      store(unit, sum, r0);
+    };
+    grid_arrive(&p.sync[1]);
+    start_stream<FMT, 3>(st, ring, a, b, warp, &lo, &hi, &next, &ld);
+    const bool ok = grid_wait(&p.sync[1], p.err, &wk.ok);
+    if (ok) {
+      if (lo < hi) st.load_h(h, st.at(lo));
+      if (tid < p.T * p.k) {  // pairs <= 256
+        const uint32_t top = __ldcg(p.hmax + tid);
+        wk.hscale[tid] = scale_up(top);
+        if (is_tiny(top)) wk.tiny = 1;
+      }
+      __syncthreads();
+      const uint32_t slot = kWindow + (uint32_t)(warp * 2048 + lane * 16);
+      if (wk.tiny)
+        run_stream<FMT, 3, true>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, slot, 512u, lanesel, rings, warp,
+                                 h, emit);
+      else
+        run_stream<FMT, 3, false>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, slot, 512u, lanesel, rings, warp,
+                                  h, emit);
     }
+    if (!ok || wk.abort) {  // copies still in flight land before the CTA leaves
+      for (int i = 0; i < ring.stages; ++i) {
+        mbar_drain(ring.full + ring.get, ring.parity);
+        ring.popped();
+      }
+      return;
+    }
+  }
+  // the last CTA to leave zeroes the words that have to be zero
+  __syncthreads();
+  if (tid == 0) wk.ok = atom_add_acq_rel(&p.sync[2], 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (wk.ok) {
+    if (tid < p.T * p.k) p.hmax[tid] = 0u;
+    if (tid < 3) p.sync[tid] = 0u;
   }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+Plan make_plan(int fmt, int T, int H) {
+  Plan q{};
+  auto up = [](uint32_t n, uint32_t a) { return (n + a - 1) / a * a; };
+  const uint32_t x = (uint32_t)((H + kDK - 1) / kDK) * 256u * (uint32_t)T;
+  q.route = x > kHBytes ? x : kHBytes;
+  q.work = up(q.route + (uint32_t)sizeof(Route), 16);
+  const uint32_t low = up(q.work + (uint32_t)sizeof(Work), 16);
+  if (fmt == 0) {
+    q.table = (kWindow + low <= 0x10000u ? 0x10000u : 0x20000u) - kWindow;
+    if (low > q.table) return q;  // no stages: refused
+    q.scratch = q.table + 128;
+    q.ring = q.table + kLut256Bytes;
+  } else {
+    q.scratch = low;
+    q.ring = low + kWarps * kScratchStride;
+  }
+  q.ring = up(kWindow + q.ring, 1024) - kWindow;  // the boxes' swizzle repeats every 512 bytes
+  const uint32_t per_stage = kWarps * kItemBytes;
+  const uint32_t fit = q.ring < kMaxWindow ? (kMaxWindow - q.ring) / per_stage : 0;
+  q.stages = (int)(fit < (uint32_t)kMaxStages ? fit : (uint32_t)kMaxStages);
+  q.total = q.ring + (uint32_t)q.stages * per_stage;
+  return q;
+}
+
 }  // namespace
 
-size_t moe_decode_workspace(int T, int k, int H, int I, size_t* count_at, size_t* part_at, size_t* h_at) {
+size_t moe_decode_workspace(int T, int k, int H, int I, size_t* at) {
   size_t n = kSyncBytes;
-  *count_at = n;
-  n = align256(n + (size_t)(H / 16) * sizeof(unsigned));
-  *part_at = n;
-  n += (size_t)kMaxGrid * 2 * 32 * sizeof(float4);
-  *h_at = n;
-  return align256(n + (size_t)T * k * ((I + kDK - 1) / kDK) * kDK * 2);
+  at[0] = n;  // hmax
+  n = align256(n + (size_t)kMaxPairs * sizeof(unsigned));
+  at[1] = n;  // unit_count
+  n = align256(n + (size_t)(H / 32) * sizeof(unsigned));
+  at[2] = n;  // part
+  n += (size_t)kMaxGrid * 2 * 2 * 32 * sizeof(float4);
+  at[3] = n;  // hbuf
+  return align256(n + (size_t)T * k * ((I + kDK - 1) / kDK) * kDK * sizeof(float));
 }
 
 template <int FMT>
-static cudaError_t launch_t(const MoeDecodeArgs& p, int num_sms, cudaStream_t stream) {
+static cudaError_t launch_t(const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p, int num_sms,
+                            cudaStream_t stream) {
   static std::atomic<bool> configured[64];
-  constexpr int kMaxSmem = 227 * 1024;
-  cudaError_t e = set_smem_limit_once(moe_decode_kernel<FMT>, kMaxSmem, configured);
+  const Plan plan = make_plan(FMT, p.T, p.H);
+  if (plan.stages < 1) return cudaErrorInvalidConfiguration;
+  cudaError_t e = set_smem_limit_once(moe_decode_kernel<FMT>, (int)kMaxWindow, configured);
   if (e != cudaSuccess) return e;
-  const uint32_t x_bytes = (uint32_t)((p.H + kDK - 1) / kDK) * 256u * (uint32_t)p.T;
-  const uint32_t table_at = kWindow + x_bytes <= 0x10000u ? 0x10000u : 0x20000u;
-  const uint32_t smem = table_at - kWindow + (uint32_t)kLut256Bytes + (uint32_t)sizeof(Tables);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(num_sms < kMaxGrid ? num_sms : kMaxGrid));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = plan.total;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // the grid barriers need every CTA resident
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_decode_kernel<FMT>, p, table_at, smem);
+  return cudaLaunchKernelEx(&cfg, moe_decode_kernel<FMT>, map1, map2, p, plan);
 }
 
-cudaError_t launch_moe_decode(int fmt, const MoeDecodeArgs& p, int num_sms, cudaStream_t stream) {
-  return fmt == 0 ? launch_t<0>(p, num_sms, stream) : launch_t<1>(p, num_sms, stream);
+cudaError_t launch_moe_decode(int fmt, const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p,
+                              int num_sms, cudaStream_t stream) {
+  return fmt == 0 ? launch_t<0>(map1, map2, p, num_sms, stream) : launch_t<1>(map1, map2, p, num_sms, stream);
 }
 
 }  // namespace gnf4
