@@ -100,17 +100,18 @@ gnf4_status check_ptr(const void* p, const char* name, size_t align, bool requir
   return GNF4_OK;
 }
 
-// check_ptr, and the memory belongs to the device the kernel will run on (managed memory belongs to all).
+// check_ptr for memory that has to belong to the current device (managed memory belongs to all): one query.
 gnf4_status check_local_ptr(const void* p, const char* name, size_t align, bool required = true) {
-  gnf4_status st = check_ptr(p, name, align, required);
-  if (st != GNF4_OK || p == nullptr) return st;
+  if (p == nullptr || reinterpret_cast<uintptr_t>(p) % align != 0) return check_ptr(p, name, align, required);
   int dev = -1;
   cudaPointerAttributes a;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaPointerGetAttributes(&a, p);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes");
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return check_ptr(p, name, align, required);
+  }
   if (a.type == cudaMemoryTypeDevice && a.device != dev)
     return fail(GNF4_ERR_INVALID_ARG, "%s is memory of device %d, the current device is %d", name, a.device, dev);
+  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return check_ptr(p, name, align, required);
   return GNF4_OK;
 }
 
@@ -1094,8 +1095,8 @@ static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w,
   GNF4_TRY(check_local_ptr(topk_ids, "topk_ids", 4));
   GNF4_TRY(check_local_ptr(topk_weights, "topk_weights", 4));
   GNF4_TRY(check_local_ptr(out, "out", 16));
-  size_t at[4];
-  const size_t need = moe_decode_workspace(T, k, H, I, at);
+  size_t at[5];
+  const size_t need = moe_decode_workspace(T, k, I, at);
   if (workspace_bytes < need)
     return fail(GNF4_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
                 need);
@@ -1117,6 +1118,7 @@ static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w,
   p.unit_count = reinterpret_cast<unsigned*>(ws + at[1]);
   p.part = reinterpret_cast<float*>(ws + at[2]);
   p.hbuf = reinterpret_cast<float*>(ws + at[3]);
+  p.h16 = reinterpret_cast<uint4*>(ws + at[4]);
   p.err = d->err;
   p.T = T, p.E = E, p.k = k, p.H = H, p.I = I;
   CUtensorMap map1, map2;
@@ -1148,8 +1150,8 @@ size_t gnf4_moe_decode_workspace_bytes(int T, int k, int H, int I) {
   if (T < 1 || T > kMoeDecodeMaxTokens || k < 1 || k > kMaxRouterTopK || H < 32 || I < 32 || I > 65536 ||
       H > kMoeDecodeMaxTH)
     return 0;
-  size_t at[4];
-  return moe_decode_workspace(T, k, H, I, at);
+  size_t at[5];
+  return moe_decode_workspace(T, k, I, at);
 }
 
 gnf4_status gnf4_moe_decode_nf4(const void* x, const void* router_w, const float* bias, float* logits, int T, int E,

@@ -186,16 +186,17 @@ struct MoeDecodeArgs {
   int* topk_ids;                  // [T, k]
   float* topk_weights;            // [T, k]
   __nv_bfloat16* out;             // [T, H]
-  unsigned* sync;                 // workspace: barrier words, zero between calls
-  unsigned* hmax;                 // workspace: largest |h| per pair (fp32 bits), zero between calls
+  unsigned* sync;                 // workspace: parity and barrier words
+  unsigned* hmax;                 // workspace: largest |h| per pair (fp32 bits), by parity
   unsigned* unit_count;           // workspace: [H/32], zero between calls
   float* part;                    // workspace: partial sums of output tiles split between CTAs
   float* hbuf;                    // workspace: [T*k, I padded to 128], in MMA fragment order
+  uint4* h16;                     // workspace: the same as scaled fp16
   unsigned* err;
   int T, E, k, H, I;
 };
-// Bytes in all; at[0..3]: where hmax, unit_count, part and hbuf begin (sync at 0).
-size_t moe_decode_workspace(int T, int k, int H, int I, size_t* at);
+// Bytes in all; at[0..4]: where hmax, unit_count, part, hbuf and h16 begin (sync at 0).
+size_t moe_decode_workspace(int T, int k, int I, size_t* at);
 // map1: w1 as [E][gate, up][I][H/2] in boxes of 64 bytes x 16 rows x both; map2: w2 as [E][H][I/2] in boxes of
 // 64 bytes x 32 rows; both with the 64-byte swizzle and zero fill.
 cudaError_t launch_moe_decode(int fmt, const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p,

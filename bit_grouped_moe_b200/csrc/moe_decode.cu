@@ -73,7 +73,8 @@ constexpr uint32_t kMaxWindow = 227 * 1024;        // dynamic shared memory of a
 struct Route {
   short row[kMaxPairs][kMaxT];  // pair = row of h of (hit expert, token); ~(a pair of the expert) if not routed
   short expert[kMaxPairs];      // hit expert ids, ascending
-  uint32_t hit[kMaxExperts / 32];
+  uint32_t hit[kMaxExperts / 32];   // bit per expert
+  uint32_t tokens[kMaxExperts / 4]; // byte per expert: the tokens that chose it
   short sel_id[kMaxPairs];      // by pair
   float sel_p[kMaxPairs];
 };
@@ -82,6 +83,7 @@ struct Work {
   float red[kWarps][kMaxT];     // router products per warp
   uint32_t xmax[kMaxT];         // largest finite |x| of a token (fp32 bits)
   float hscale[kMaxPairs];      // scale of a pair's fp16 h
+  uint32_t htop[kMaxPairs];     // largest finite |h| of a pair in this CTA (fp32 bits)
   int nhit;
   int tiny;                     // a pair's h lies below 2^kTinyExp throughout
   int ok;
@@ -101,6 +103,7 @@ __device__ __forceinline__ bool is_tiny(uint32_t top) { return top != 0u && top 
 // 0x20000 where x needs the room); then the rings.
 struct Plan {
   uint32_t route, work, scratch, table, ring, total;
+  uint32_t act;  // bytes for activations at the start
   int stages;
 };
 
@@ -112,8 +115,11 @@ template <int FMT>
 __device__ __forceinline__ constexpr int scratch_row(int r) {
   return FMT == 0 ? (r >> 4) * 256 + (r & 15) * 8 : 16 * r;
 }
-constexpr uint32_t kHBytes = kThreads * 64;     // phase 3: h of one item
-constexpr int kSyncBytes = 256;      // workspace: words 0, 1 = grid barriers, 2 = CTAs that have left; then hmax
+constexpr uint32_t kHBytes = kThreads * 64;  // phase 3: h of one item
+// Workspace words: [0] parity of the call, [1 + b + 3 * parity] arrivals at grid barrier b.  A call uses the counters
+// (and the hmax) of its parity and zeroes the other ones, which the call before it used; no CTA has to wait for the
+// others to leave.
+constexpr int kSyncBytes = 256;
 
 // NF4 pairs as fp16, one copy per lane, 256 bytes per entry.
 __device__ __forceinline__ void build_table(uint32_t* lut, int tid) {
@@ -275,7 +281,8 @@ __device__ __forceinline__ uint32_t score_key(float f) {
 // lower expert, NaN last) and the softmax of their raw logits, as the router
 // epilogue of the routing call.  A lane holds the keys of N experts.
 template <int N>
-__device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Route& s, int t, int lane) {
+__device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Route& s, int t, int lane,
+                                            float* logit) {
   const float* logits = p.logits + (size_t)t * p.E;
   uint32_t key[N];
   float raw[N];
@@ -316,6 +323,17 @@ __device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Route& s, in
       l = v;
     }
   }
+  if (lane < p.k) {
+    s.sel_id[t * p.k + lane] = (short)mine;
+    atomicOr(&s.hit[mine >> 5], 1u << (mine & 31));
+    atomicOr(&s.tokens[mine >> 2], 1u << (8 * (mine & 3) + t));
+    if (blockIdx.x == 0) p.topk_ids[t * p.k + lane] = mine;
+  }
+  *logit = l;
+}
+
+// The weights of the selected logits: the other half of select_topk, off the path to the first loads.
+__device__ __forceinline__ void weigh_topk(const MoeDecodeArgs& p, Route& s, int t, int lane, float l) {
   float m = l;  // a NaN logit makes every weight NaN
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
@@ -327,47 +345,30 @@ __device__ __forceinline__ void select_topk(const MoeDecodeArgs& p, Route& s, in
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane < p.k) {
-    const float w = ex / sum;
-    s.sel_id[t * p.k + lane] = (short)mine;
-    s.sel_p[t * p.k + lane] = w;
-    atomicOr(&s.hit[mine >> 5], 1u << (mine & 31));
-    if (blockIdx.x == 0) {
-      p.topk_ids[t * p.k + lane] = mine;
-      p.topk_weights[t * p.k + lane] = w;
-    }
+    s.sel_p[t * p.k + lane] = ex / sum;
+    if (blockIdx.x == 0) p.topk_weights[t * p.k + lane] = ex / sum;
   }
 }
 
-// Hit experts in ascending order, and the pair of every (hit expert, token).  All threads.
+// Hit experts in ascending order, and the pair of every (hit expert, token).  All threads; a barrier before and after.
 __device__ __forceinline__ void list_hits(const MoeDecodeArgs& p, Route& s, int* nhit, int tid) {
-  // rank of expert e = set bits below it
-  auto rank = [&](int e) {
-    int r = __popc(s.hit[e >> 5] & ((1u << (e & 31)) - 1u));
+  if (tid >= kThreads - 32) {
+    const int n = __reduce_add_sync(0xffffffffu, (unsigned)__popc(s.hit[tid & 31]));
+    if (tid == kThreads - 32) *nhit = n;
+  }
+  if (tid < p.T * p.k) {  // pairs <= 256
+    const int e = s.sel_id[tid], tok = tid / p.k;
+    int r = __popc(s.hit[e >> 5] & ((1u << (e & 31)) - 1u));  // rank: set bits below e
     for (int i = 0; i < (e >> 5); ++i) r += __popc(s.hit[i]);
-    return r;
-  };
-  const int pairs = p.T * p.k;
-  for (int i = tid; i < pairs * kMaxT; i += kThreads) s.row[i / kMaxT][i % kMaxT] = -1;
-  if (tid == kThreads - 1) {
-    int n = 0;
-    for (int i = 0; i < (p.E + 31) / 32; ++i) n += __popc(s.hit[i]);
-    *nhit = n;
+    const uint32_t toks = (s.tokens[e >> 2] >> (8 * (e & 3))) & 255u;
+    s.row[r][tok] = (short)tid;
+    if (tok == __ffs((int)toks) - 1) {  // the expert's first token fills in for those that did not choose it
+      s.expert[r] = (short)e;
+#pragma unroll
+      for (int t = 0; t < kMaxT; ++t)
+        if (!((toks >> t) & 1u)) s.row[r][t] = (short)~tid;
+    }
   }
-  __syncthreads();
-  if (tid < pairs) {  // pairs <= 256
-    const int e = s.sel_id[tid], r = rank(e);
-    s.expert[r] = (short)e;  // the same value from every pair of the expert
-    s.row[r][tid / p.k] = (short)tid;
-  }
-  __syncthreads();
-  if (tid < *nhit) {
-    short any = 0;
-    for (int t = 0; t < p.T; ++t)
-      if (s.row[tid][t] >= 0) any = s.row[tid][t];
-    for (int t = 0; t < kMaxT; ++t)
-      if (s.row[tid][t] < 0) s.row[tid][t] = (short)~any;
-  }
-  __syncthreads();
 }
 
 // ---------------------------------------------------------------- item stream
@@ -603,23 +604,18 @@ struct Stream {
     const int r = s.row[ei][g];
     return r < 0 ? ~r : r;
   }
-  __device__ __forceinline__ void load_h(float4 (&h)[8], const Cursor& c) const {
-    const float4* q = reinterpret_cast<const float4*>(p.hbuf) + (((size_t)pair(c.ei) * nd + c.d) * 16 + t) * 2;
+  // Phase 3 with h in global memory: this lane's fp16 h of an item, and to its slot.
+  __device__ __forceinline__ void load_h(uint4 (&h)[4], const Cursor& c) const {
+    const uint4* q = p.h16 + ((size_t)pair(c.ei) * nd + c.d) * 16 + t;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __ldcg(q + 8 * (i >> 1) + (i & 1));
+    for (int i = 0; i < 4; ++i) h[i] = __ldcg(q + 4 * i);
   }
-  __device__ __forceinline__ void store_h(uint32_t slot, const float4 (&h)[8], const Cursor& c) const {
-    const float sc = wk.hscale[pair(c.ei)];
+  __device__ __forceinline__ void store_h(uint32_t slot, const uint4 (&h)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 a = h[2 * i], b = h[2 * i + 1];
-      __half2 v[4] = {__floats2half2_rn(a.x * sc, a.y * sc), __floats2half2_rn(a.z * sc, a.w * sc),
-                      __floats2half2_rn(b.x * sc, b.y * sc), __floats2half2_rn(b.z * sc, b.w * sc)};
-      const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(slot + 512 * i), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                   "r"(u[3])
+    for (int i = 0; i < 4; ++i)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(slot + 512 * i), "r"(h[i].x), "r"(h[i].y),
+                   "r"(h[i].z), "r"(h[i].w)
                    : "memory");
-    }
   }
   // 1 / the scale of column q (0, 1) of this lane; 0 for a phase 3 column whose token did not choose expert ei.
   __device__ __forceinline__ float unit_of(int ei, int q) const {
@@ -647,40 +643,87 @@ struct Ring {
   }
 };
 
-// Streams the CTA's items [a, b): `ready` runs once the first loads are in
-// flight (a barrier may hide behind them), `emit(unit, acc, whole)` is called
-// by one full warp per unit of the range, whole = all of its items were here.
-// x: phase 2 this lane's x in shared memory (items 4 * x_step apart), phase 3
-// its slot for h.  A wait that gives up flags the timeout; the stream then runs
-// to its end on whatever the ring holds.
-template <int FMT, int PHASE, bool TINY, class Emit>
-__device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Work& wk, unsigned* err, int a,
-                                           int b, int lo, int hi, int next, Cursor ld, uint32_t scratch, uint32_t x,
-                                           uint32_t x_step, uint32_t lanesel, uint8_t* rings, int warp, float4 (&h)[8],
-                                           Emit emit) {
-  const int n = b - a, per = st.per, lane = st.lane;
-  auto split = [&](int w) { return a + n * w / kWarps; };
+// Waits for a box; the rare second look is kept out of the loop.
+__device__ __noinline__ void box_wait_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+  mbar_wait(bar, parity, err, abort);
+}
+
+// A warp's way through its items [lo, hi) of the CTA's [a, b).
+template <int FMT>
+struct Walk {
+  int a, b, lo, hi;
+  int next;         // next item to issue
+  Cursor cur, ld;   // next item to multiply, next item to issue
+  const uint8_t* row;   // this lane's scales of the rows at cur (of the group loaded last)
+  ScaleGroup<FMT> sc;   // the scale group after the one in the scratch
+};
+
+template <int FMT, int PHASE>
+__device__ __forceinline__ void issue_box(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w) {
+  if (w.next < w.hi) {
+    if (st.lane == 0) st.load_box(ring.ptr + ring.put * kItemBytes, ring.full + ring.put, w.ld);
+    ring.pushed();
+    ++w.next;
+    st.advance(w.ld);
+  }
+}
+
+// The first boxes and scales on their way.
+template <int FMT, int PHASE>
+__device__ __forceinline__ void start_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, int a, int b,
+                                             int warp) {
+  const int n = b - a;
+  w.a = a, w.b = b;
+  w.lo = a + n * warp / kWarps;
+  w.hi = a + n * (warp + 1) / kWarps;
+  w.next = w.lo;
+  w.cur = w.ld = st.at(w.lo);
+  // earlier generic accesses to the ring (partial sums) before the boxes
+  fence_proxy_async_smem();
+  __syncwarp();
+  for (int i = 0; i < ring.stages; ++i) issue_box(st, ring, w);
+  if (w.lo < w.hi) {
+    w.row = st.scale_row(w.cur);
+    load_scales<FMT>(w.sc, w.row, st.srow, w.cur.d >> 2);
+  }
+}
+
+// The loaded scale group (the one of item `item` at cur) to the scratch, and the one after it on its way.
+template <int FMT, int PHASE>
+__device__ __forceinline__ void next_scales(const Stream<FMT, PHASE>& st, Walk<FMT>& w, int item, uint32_t scratch) {
+  const int group = w.cur.d >> 2;
+  scales_to_scratch<FMT>(w.sc, st.ns - group * (FMT == 0 ? 8 : 16), scratch, st.lane);
+  const int skip = min(4 - (w.cur.d & 3), st.nd - w.cur.d);
+  if (item + skip >= w.hi) return;  // no other group belongs to this warp
+  if (w.cur.d + skip < st.nd) {
+    load_scales<FMT>(w.sc, w.row, st.srow, group + 1);
+  } else {
+    Cursor q = w.cur;
+    q.d = st.nd - 1;
+    st.advance(q);
+    w.row = st.scale_row(q);
+    load_scales<FMT>(w.sc, w.row, st.srow, 0);
+  }
+}
+
+// Multiplies the warp's items.  The first scale group lies in the scratch;
+// phase 3: h holds the first item's activations.  `emit(unit, acc, whole)` is
+// called by one full warp per unit of the CTA's range, whole = all of its items
+// were here.  x: phase 2 this lane's x in shared memory (items 4 * x_step
+// apart); phase 3 this lane's column of h in shared memory (HERE), else its
+// slot for the h of one item.  A wait that gives up flags the timeout; the
+// stream then runs to its end on whatever the ring holds.
+template <int FMT, int PHASE, bool TINY, bool HERE, class Emit>
+__device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, Work& wk,
+                                           unsigned* err, uint32_t scratch, uint32_t x, uint32_t x_step,
+                                           uint32_t lanesel, uint8_t* rings, int warp, uint4 (&h)[4], Emit emit) {
+  const int a = w.a, b = w.b, lo = w.lo, hi = w.hi, per = st.per, lane = st.lane;
+  auto split = [&](int i) { return a + (b - a) * i / kWarps; };
   // NF4 reads 8 bytes per lane: this order of the 8 rows keeps each half of the warp on 32 banks
   const int r0 = FMT == 0 ? (st.g & 1) | ((st.g & 2) << 1) | ((st.g & 4) >> 1) : st.g;
-  Cursor cur = st.at(lo);
-  ScaleGroup<FMT> sc;
-  // the group after the one at c, if it belongs to this warp (item: index of c)
-  auto load_next_group = [&](const Cursor& c, int item) {
-    const int skip = min(4 - (c.d & 3), st.nd - c.d);
-    if (item + skip >= hi) return;
-    Cursor q = c;
-    if (q.d + skip < st.nd) {
-      q.d += skip;
-    } else {
-      q.d = st.nd - 1;
-      st.advance(q);
-    }
-    load_scales<FMT>(sc, st.scale_row(q), st.srow, q.d >> 2);
-  };
-  if (lo < hi) {
-    load_scales<FMT>(sc, st.scale_row(cur), st.srow, cur.d >> 2);
-    if (PHASE == 3) st.store_h(x, h, cur);
-  }
+  if (!HERE && lo < hi) st.store_h(x, h);
+  uint32_t column = x;  // phase 3, HERE: the current expert's row of h
+  if (PHASE == 3 && HERE && lo < hi) column = x + 256u * (uint32_t)(st.pair(w.cur.ei) * st.nd);
   float acc[2][4] = {};
   float one[2][4] = {};   // phase 3: the current expert's part
   float head[2][4] = {};  // a unit begun by an earlier warp
@@ -688,30 +731,21 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
   if (PHASE == 2) unit2[0] = st.unit_of(0, 0), unit2[1] = st.unit_of(0, 1);
   bool tail = false;  // a unit begun by this warp and not finished by it
   for (int item = lo; item < hi; ++item) {
-    if (item == lo || (cur.d & 3) == 0) {
-      scales_to_scratch<FMT>(sc, st.ns - (cur.d >> 2) * (FMT == 0 ? 8 : 16), scratch, lane);
-      load_next_group(cur, item);
-    }
-    const int unit = cur.unit, ei = cur.ei;
-    const uint32_t sa = scratch + (cur.d & 3) * kScratchItem;
-    const uint32_t xa = PHASE == 2 ? x + 4 * x_step * cur.d : x;
-    const bool turn = st.advance(cur), more = item + 1 < hi;
-    if (PHASE == 3 && more) st.load_h(h, cur);
+    const int unit = w.cur.unit, ei = w.cur.ei, d = w.cur.d;
+    if ((d & 3) == 0 && item > lo) next_scales<FMT, PHASE>(st, w, item, scratch);
+    const bool turn = st.advance(w.cur), more = item + 1 < hi;
+    if (!HERE && more) st.load_h(h, w.cur);
     if (PHASE == 3 && TINY) unit2[0] = st.unit_of(ei, 0), unit2[1] = st.unit_of(ei, 1);
-    mbar_wait(ring.full + ring.get, ring.parity, err, &wk.abort);
+    if (!mbar_try_wait(ring.full + ring.get, ring.parity))
+      box_wait_slow(ring.full + ring.get, ring.parity, err, &wk.abort);
     __syncwarp();
-    multiply<FMT, TINY, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(PHASE == 3 ? one : acc,
-                                                                ring.base + ring.get * kItemBytes, sa, xa, x_step,
-                                                                unit2, r0, st.t, lanesel);
+    multiply<FMT, TINY, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(
+        PHASE == 3 ? one : acc, ring.base + ring.get * kItemBytes, scratch + (d & 3) * kScratchItem,
+        HERE ? column + 4 * x_step * d : x, x_step, unit2, r0, st.t, lanesel);
     ring.popped();
     __syncwarp();  // every lane has read the box and the scratch
-    if (next < hi) {
-      if (lane == 0) st.load_box(ring.ptr + ring.put * kItemBytes, ring.full + ring.put, ld);
-      ring.pushed();
-      ++next;
-      st.advance(ld);
-    }
-    if (PHASE == 3 && more) st.store_h(x, h, cur);
+    issue_box(st, ring, w);
+    if (!HERE && more) st.store_h(x, h);
     if (!turn && more) continue;
     if (PHASE == 3) {
       // columns of tokens that did not choose the expert are dropped, not
@@ -726,8 +760,9 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
           one[k][q] = one[k][q + 2] = 0.f;
         }
       }
+      if (HERE) column = x + 256u * (uint32_t)(st.pair(w.cur.ei) * st.nd);
     }
-    if (more && cur.unit == unit) continue;
+    if (more && w.cur.unit == unit) continue;
     const int first = max(unit * per, a), last = min((unit + 1) * per, b);  // the unit's items in this CTA
     if (lo <= first && last <= hi) {
       emit(unit, acc, last - first == per, r0, unit2);
@@ -744,42 +779,22 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
     for (int k = 0; k < 2; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
   }
   // the ring is idle: its first KB takes the head part
-  auto part = [&](int w) { return reinterpret_cast<float4*>(rings + (size_t)w * ring.stages * kItemBytes) + lane; };
+  auto part = [&](int i) { return reinterpret_cast<float4*>(rings + (size_t)i * ring.stages * kItemBytes) + lane; };
 #pragma unroll
   for (int k = 0; k < 2; ++k) part(warp)[32 * k] = make_float4(head[k][0], head[k][1], head[k][2], head[k][3]);
   __syncthreads();
   if (tail) {  // add the parts of the warps after this one
     const int unit = (hi - 1) / per;
     const int first = max(unit * per, a), last = min((unit + 1) * per, b);
-    for (int w = warp + 1; w < kWarps && split(w) < last; ++w) {
-      if (split(w) == split(w + 1)) continue;
+    for (int i = warp + 1; i < kWarps && split(i) < last; ++i) {
+      if (split(i) == split(i + 1)) continue;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 v = part(w)[32 * k];
+        const float4 v = part(i)[32 * k];
         acc[k][0] += v.x, acc[k][1] += v.y, acc[k][2] += v.z, acc[k][3] += v.w;
       }
     }
     emit(unit, acc, last - first == per, r0, unit2);
-  }
-}
-
-// A warp's items of the CTA's [a, b), and the first boxes on their way.
-template <int FMT, int PHASE>
-__device__ __forceinline__ void start_stream(const Stream<FMT, PHASE>& st, Ring& ring, int a, int b, int warp, int* lo,
-                                             int* hi, int* next, Cursor* ld) {
-  const int n = b - a;
-  *lo = a + n * warp / kWarps;
-  *hi = a + n * (warp + 1) / kWarps;
-  *ld = st.at(*lo);
-  *next = *lo;
-  // earlier generic accesses to the ring (partial sums) before the boxes
-  fence_proxy_async_smem();
-  __syncwarp();
-  for (int i = 0; i < ring.stages && *next < *hi; ++i) {
-    if (st.lane == 0) st.load_box(ring.ptr + ring.put * kItemBytes, ring.full + ring.put, *ld);
-    ring.pushed();
-    ++*next;
-    st.advance(*ld);
   }
 }
 
@@ -847,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ring.stages = plan.stages;
 
   if (tid < kMaxExperts / 32) rt.hit[tid] = 0u;
+  if (tid < kMaxExperts / 4) rt.tokens[tid] = 0u;
   if (tid < kMaxT) wk.xmax[tid] = 0u;
   if (tid == 0) {
     wk.abort = 0;
@@ -856,6 +872,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane < plan.stages) mbar_init(ring.full + lane, 1);
   fence_mbar_init();
+  if (tid < kMaxPairs) wk.htop[tid] = 0u;
+  const unsigned parity = __ldcg(p.sync) & 1u;
+  unsigned* const barrier = p.sync + 1 + 3 * parity;
+  unsigned* const hmax = p.hmax + kMaxPairs * parity;
   // the table and x are laid out while the router's first weights arrive
   const RouterPart part(p, tid);
   __syncthreads();
@@ -866,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (p.T == 2) router_product<2>(p, wk, part, tid);
     else if (p.T <= 4) router_product<4>(p, wk, part, tid);
     else router_product<8>(p, wk, part, tid);
-    grid_arrive(&p.sync[0]);
+    grid_arrive(barrier);
   }
   const int nd2 = (p.I + kDK - 1) / kDK;
   if (p.I % kDK != 0) {  // the last item of every row of h: zero past I
@@ -878,29 +898,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             make_float4(0.f, 0.f, 0.f, 0.f);
       }
   }
+  if (blockIdx.x == gridDim.x - 1) {  // what the call before this one used
+    if (tid < 3) p.sync[1 + 3 * (1u - parity) + tid] = 0u;
+    if (tid < kMaxPairs) p.hmax[kMaxPairs * (1u - parity) + tid] = 0u;
+  }
   if (p.router_w != nullptr) {
-    if (!grid_wait(&p.sync[0], p.err, &wk.ok)) return;
+    if (!grid_wait(barrier, p.err, &wk.ok)) return;
   } else {
     __syncthreads();
   }
+  float logit = 0.f;  // warp t, lane j: the j-th selected logit of token t
   if (warp < p.T) {
-    if (p.E <= 64) select_topk<2>(p, rt, warp, lane);
-    else if (p.E <= 128) select_topk<4>(p, rt, warp, lane);
-    else if (p.E <= 384) select_topk<12>(p, rt, warp, lane);
-    else select_topk<kMaxExperts / 32>(p, rt, warp, lane);
+    if (p.E <= 64) select_topk<2>(p, rt, warp, lane, &logit);
+    else if (p.E <= 128) select_topk<4>(p, rt, warp, lane, &logit);
+    else if (p.E <= 384) select_topk<12>(p, rt, warp, lane, &logit);
+    else select_topk<kMaxExperts / 32>(p, rt, warp, lane, &logit);
   }
   __syncthreads();
   list_hits(p, rt, &wk.nhit, tid);
+  __syncthreads();
   const uint32_t lanesel = (uint32_t)lane * 4u | ((kWindow + plan.table) & 0x00FF0000u);
-  int lo, hi, next;
-  Cursor ld;
-  float4 h[8] = {};  // phase 3: the next item's activations on their way
+  Walk<FMT> w;
+  uint4 h[4];  // phase 3: the next item's activations on their way
 
   {  // gate_up + SwiGLU; h times its router weight goes to the workspace in fragment order
     const Stream<FMT, 2> st(p, rt, wk, &map1, lane);
     const Share sh(wk.nhit * st.cols, gridDim.x);
-    const int a = sh.begin(blockIdx.x) * st.per, b = sh.begin(blockIdx.x + 1) * st.per;
-    start_stream<FMT, 2>(st, ring, a, b, warp, &lo, &hi, &next, &ld);
+    start_stream<FMT, 2>(st, ring, w, sh.begin(blockIdx.x) * st.per, sh.begin(blockIdx.x + 1) * st.per, warp);
+    if (warp < p.T) weigh_topk(p, rt, warp, lane, logit);
+    __syncthreads();
+    if (w.lo < w.hi) next_scales<FMT, 2>(st, w, w.lo, scratch);
     bool tiny = false;
     for (int i = 0; i < p.T; ++i) tiny |= is_tiny(wk.xmax[i]);
     // columns past T repeat the last token and are never stored
@@ -924,20 +951,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (r >= 0 && g == 0) atomicMax(p.hmax + r, top);
+        if (r >= 0 && g == 0) atomicMax(&wk.htop[r], top);
       }
     };
     if (tiny)
-      run_stream<FMT, 2, true>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, x, x_step, lanesel, rings, warp, h,
-                               emit);
+      run_stream<FMT, 2, true, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit);
     else
-      run_stream<FMT, 2, false>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, x, x_step, lanesel, rings, warp, h,
-                                emit);
+      run_stream<FMT, 2, false, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit);
   }
   {  // down + combine
     const Stream<FMT, 3> st(p, rt, wk, &map2, lane);
     const Share sh((p.H / 32) * st.per, gridDim.x);
-    const int a = sh.begin(blockIdx.x), b = sh.begin(blockIdx.x + 1);
     auto store = [&](int unit, const float(&acc)[2][4], int r0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -969,6 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (!last) return;
       float sum[2][4] = {};
+#pragma unroll 4
       for (int c = c0; c <= c1; ++c)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -977,50 +1002,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       store(unit, sum, r0);
     };
-    grid_arrive(&p.sync[1]);
-    start_stream<FMT, 3>(st, ring, a, b, warp, &lo, &hi, &next, &ld);
-    const bool ok = grid_wait(&p.sync[1], p.err, &wk.ok);
+    __syncthreads();
+    // one maximum per pair and CTA: thousands of them on a few lines delayed the barrier by 6 us
+    if (tid < p.T * p.k && wk.htop[tid] != 0u) atomicMax(hmax + tid, wk.htop[tid]);
+    grid_arrive(barrier + 1);
+    // the weights do not wait for the other CTAs
+    start_stream<FMT, 3>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
+    if (w.lo < w.hi) next_scales<FMT, 3>(st, w, w.lo, scratch);
+    bool ok = grid_wait(barrier + 1, p.err, &wk.ok);
     if (ok) {
-      if (lo < hi) st.load_h(h, st.at(lo));
-      if (tid < p.T * p.k) {  // pairs <= 256
-        const uint32_t top = __ldcg(p.hmax + tid);
+      if (blockIdx.x == 0 && tid == 0) p.sync[0] = 1u - parity;  // every CTA has read it
+      const int pairs = p.T * p.k;  // <= 256
+      if (tid < pairs) {
+        const uint32_t top = __ldcg(hmax + tid);
         wk.hscale[tid] = scale_up(top);
         if (is_tiny(top)) wk.tiny = 1;
       }
       __syncthreads();
-      const uint32_t slot = kWindow + (uint32_t)(warp * 2048 + lane * 16);
-      if (wk.tiny)
-        run_stream<FMT, 3, true>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, slot, 512u, lanesel, rings, warp,
-                                 h, emit);
-      else
-        run_stream<FMT, 3, false>(st, ring, wk, p.err, a, b, lo, hi, next, ld, scratch, slot, 512u, lanesel, rings, warp,
-                                  h, emit);
+      // h to fp16: all of it into every CTA's shared memory, or, where that is
+      // too small, each CTA a share in global memory and one more barrier
+      const float4* src = reinterpret_cast<const float4*>(p.hbuf);
+      const int chunks = pairs * nd2 * 16;  // of 8 values
+      const bool here = (uint32_t)chunks * 16u <= plan.act;
+      for (int i = here ? tid : (int)(blockIdx.x * kThreads) + tid; i < chunks; i += here ? kThreads : (int)gridDim.x * kThreads) {
+        const float4 u = __ldcg(src + 2 * i), v = __ldcg(src + 2 * i + 1);
+        const float sc = wk.hscale[i / (nd2 * 16)];
+        __half2 q[4] = {__floats2half2_rn(u.x * sc, u.y * sc), __floats2half2_rn(u.z * sc, u.w * sc),
+                        __floats2half2_rn(v.x * sc, v.y * sc), __floats2half2_rn(v.z * sc, v.w * sc)};
+        *(here ? reinterpret_cast<uint4*>(smem_raw) + i : p.h16 + i) = *reinterpret_cast<uint4*>(q);
+      }
+      if (here) {
+        __syncthreads();
+        const uint32_t x = kWindow + 16u * (uint32_t)t;
+        if (wk.tiny)
+          run_stream<FMT, 3, true, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
+        else
+          run_stream<FMT, 3, false, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
+      } else {
+        grid_arrive(barrier + 2);
+        ok = grid_wait(barrier + 2, p.err, &wk.ok);
+        if (ok) {
+          if (w.lo < w.hi) st.load_h(h, w.cur);
+          const uint32_t slot = kWindow + (uint32_t)(warp * 2048 + lane * 16);
+          if (wk.tiny)
+            run_stream<FMT, 3, true, false>(st, ring, w, wk, p.err, scratch, slot, 512u, lanesel, rings, warp, h, emit);
+          else
+            run_stream<FMT, 3, false, false>(st, ring, w, wk, p.err, scratch, slot, 512u, lanesel, rings, warp, h, emit);
+        }
+      }
     }
     if (!ok || wk.abort) {  // copies still in flight land before the CTA leaves
       for (int i = 0; i < ring.stages; ++i) {
         mbar_drain(ring.full + ring.get, ring.parity);
         ring.popped();
       }
-      return;
     }
-  }
-  // the last CTA to leave zeroes the words that have to be zero
-  __syncthreads();
-  if (tid == 0) wk.ok = atom_add_acq_rel(&p.sync[2], 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (wk.ok) {
-    if (tid < p.T * p.k) p.hmax[tid] = 0u;
-    if (tid < 3) p.sync[tid] = 0u;
   }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-Plan make_plan(int fmt, int T, int H) {
+Plan make_plan(int fmt, int T, int H, int pairs, int I) {
   Plan q{};
   auto up = [](uint32_t n, uint32_t a) { return (n + a - 1) / a * a; };
   const uint32_t x = (uint32_t)((H + kDK - 1) / kDK) * 256u * (uint32_t)T;
-  q.route = x > kHBytes ? x : kHBytes;
+  // room for all of h where it is cheap: up to 64 KB without a larger x
+  const uint32_t h = (uint32_t)pairs * (uint32_t)((I + kDK - 1) / kDK) * 256u;
+  const uint32_t limit = fmt == 0 ? 32768u : 65536u;
+  q.act = x > kHBytes ? x : kHBytes;
+  if (h > q.act && h <= limit) q.act = h;
+  q.route = q.act;
   q.work = up(q.route + (uint32_t)sizeof(Route), 16);
   const uint32_t low = up(q.work + (uint32_t)sizeof(Work), 16);
   if (fmt == 0) {
@@ -1042,23 +1093,25 @@ Plan make_plan(int fmt, int T, int H) {
 
 }  // namespace
 
-size_t moe_decode_workspace(int T, int k, int H, int I, size_t* at) {
+size_t moe_decode_workspace(int T, int k, int I, size_t* at) {
   size_t n = kSyncBytes;
   at[0] = n;  // hmax
-  n = align256(n + (size_t)kMaxPairs * sizeof(unsigned));
+  n = align256(n + 2 * (size_t)kMaxPairs * sizeof(unsigned));
   at[1] = n;  // unit_count
-  n = align256(n + (size_t)(H / 32) * sizeof(unsigned));
+  n = align256(n + (size_t)(kMoeDecodeMaxTH / 32) * sizeof(unsigned));  // the same place for every shape: it stays zero
   at[2] = n;  // part
   n += (size_t)kMaxGrid * 2 * 2 * 32 * sizeof(float4);
   at[3] = n;  // hbuf
-  return align256(n + (size_t)T * k * ((I + kDK - 1) / kDK) * kDK * sizeof(float));
+  n = align256(n + (size_t)T * k * ((I + kDK - 1) / kDK) * kDK * sizeof(float));
+  at[4] = n;  // h16
+  return align256(n + (size_t)T * k * ((I + kDK - 1) / kDK) * kDK * 2);
 }
 
 template <int FMT>
 static cudaError_t launch_t(const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p, int num_sms,
                             cudaStream_t stream) {
   static std::atomic<bool> configured[64];
-  const Plan plan = make_plan(FMT, p.T, p.H);
+  const Plan plan = make_plan(FMT, p.T, p.H, p.T * p.k, p.I);
   if (plan.stages < 1) return cudaErrorInvalidConfiguration;
   cudaError_t e = set_smem_limit_once(moe_decode_kernel<FMT>, (int)kMaxWindow, configured);
   if (e != cudaSuccess) return e;

@@ -529,10 +529,10 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
  *   out           bf16 [T, H] OUT;
  *   workspace     device memory of gnf4_moe_decode_workspace_bytes(T, k, H, I)
  *                 bytes or more, zero-filled once by the caller before its
- *                 first use.  Every call that ends without a device error
- *                 leaves its counters zero, so it may be used again by calls
- *                 of any shape it is large enough for, and captured in a
- *                 graph.  After a device error zero it again.  Calls
+ *                 first use on a device.  Every call that ends without a
+ *                 device error leaves it ready for the next, of any shape it
+ *                 is large enough for, captured in a graph or not.  After a
+ *                 device error zero it again.  Calls
  *                 that may overlap on the GPU (two streams, two graphs) need a
  *                 workspace each.
  * Rules: 0 <= T <= 8, 1 <= E <= 1024, 1 <= k <= min(E, 32), H and I multiples
