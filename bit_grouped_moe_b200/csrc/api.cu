@@ -1130,11 +1130,11 @@ static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w,
     cuuint64_t strides1[3] = {r1, (cuuint64_t)I * r1, 2 * (cuuint64_t)I * r1}, strides2[2] = {r2, (cuuint64_t)H * r2};
     cuuint32_t box1[4] = {64, 16, 2, 1}, box2[3] = {64, 32, 1}, estr[4] = {1, 1, 1, 1};
     CUresult r = fn(&map1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(w_gate_up), dims1, strides1, box1, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS)
       r = fn(&map2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w_down), dims2, strides2, box2, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(GNF4_ERR_CUDA, "expert stack tensor map encode failed (CUresult %d)", (int)r);
   }

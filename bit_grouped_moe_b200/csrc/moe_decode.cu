@@ -120,6 +120,7 @@ constexpr uint32_t kHBytes = kThreads * 64;  // phase 3: h of one item
 // (and the hmax) of its parity and zeroes the other ones, which the call before it used; no CTA has to wait for the
 // others to leave.
 constexpr int kSyncBytes = 256;
+constexpr int kHmaxStep = 32;  // words: a line for every pair's maximum, so that the CTAs' updates do not queue
 
 // NF4 pairs as fp16, one copy per lane, 256 bytes per entry.
 __device__ __forceinline__ void build_table(uint32_t* lut, int tid) {
@@ -244,7 +245,7 @@ __device__ __forceinline__ void router_product(const MoeDecodeArgs& p, Work& s, 
   for (int t = 0; t < TP; ++t) acc[t] = 0.f;
   if (e < p.E) {
     const uint4* w = reinterpret_cast<const uint4*>(p.router_w) + (size_t)e * H8;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = part.first; i < H8; i += wpe * 32) {
       const uint4 wv = i == part.first ? part.w : ldg_nc_u128(w + i);
       uint4 xv[TP];
@@ -786,12 +787,21 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
   if (tail) {  // add the parts of the warps after this one
     const int unit = (hi - 1) / per;
     const int first = max(unit * per, a), last = min((unit + 1) * per, b);
-    for (int i = warp + 1; i < kWarps && split(i) < last; ++i) {
-      if (split(i) == split(i + 1)) continue;
+    // a warp without items has an empty head part: the sum runs over four warps' parts at a time
+#pragma unroll 1
+    for (int i = warp + 1; i < kWarps && split(i) < last; i += 4) {
+      float4 v[4][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float4 v = part(i)[32 * k];
-        acc[k][0] += v.x, acc[k][1] += v.y, acc[k][2] += v.z, acc[k][3] += v.w;
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) v[j][k] = part(min(i + j, kWarps - 1))[32 * k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j >= kWarps || split(i + j) >= last) break;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          acc[k][0] += v[j][k].x, acc[k][1] += v[j][k].y, acc[k][2] += v[j][k].z, acc[k][3] += v[j][k].w;
+        }
       }
     }
     emit(unit, acc, last - first == per, r0, unit2);
@@ -808,7 +818,7 @@ __device__ __forceinline__ void stage_x(const MoeDecodeArgs& p, Work& s, uint4* 
   const uint4* x = reinterpret_cast<const uint4*>(p.x) + (size_t)tok * H8;
   if (tok < p.T) {
     uint32_t m = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int i = first; i < H8; i += step) {
       const uint4 v = __ldg(x + i);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -824,7 +834,7 @@ __device__ __forceinline__ void stage_x(const MoeDecodeArgs& p, Work& s, uint4* 
   __syncthreads();
   if (tok >= p.T) return;
   const float sc = scale_up(s.xmax[tok]);
-#pragma unroll 8
+#pragma unroll 4
   for (int i = first; i < nd * 16; i += step) {
     uint4 v = i < H8 ? __ldg(x + i) : make_uint4(0u, 0u, 0u, 0u);
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -875,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < kMaxPairs) wk.htop[tid] = 0u;
   const unsigned parity = __ldcg(p.sync) & 1u;
   unsigned* const barrier = p.sync + 1 + 3 * parity;
-  unsigned* const hmax = p.hmax + kMaxPairs * parity;
+  unsigned* const hmax = p.hmax + kMaxPairs * kHmaxStep * parity;
   // the table and x are laid out while the router's first weights arrive
   const RouterPart part(p, tid);
   __syncthreads();
@@ -900,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (blockIdx.x == gridDim.x - 1) {  // what the call before this one used
     if (tid < 3) p.sync[1 + 3 * (1u - parity) + tid] = 0u;
-    if (tid < kMaxPairs) p.hmax[kMaxPairs * (1u - parity) + tid] = 0u;
+    if (tid < kMaxPairs) p.hmax[kHmaxStep * (kMaxPairs * (1u - parity) + tid)] = 0u;
   }
   if (p.router_w != nullptr) {
     if (!grid_wait(barrier, p.err, &wk.ok)) return;
@@ -925,9 +935,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Stream<FMT, 2> st(p, rt, wk, &map1, lane);
     const Share sh(wk.nhit * st.cols, gridDim.x);
     start_stream<FMT, 2>(st, ring, w, sh.begin(blockIdx.x) * st.per, sh.begin(blockIdx.x + 1) * st.per, warp);
-    if (warp < p.T) weigh_topk(p, rt, warp, lane, logit);
-    __syncthreads();
+    if (warp < p.T) weigh_topk(p, rt, warp, lane, logit);  // while the first weights arrive
     if (w.lo < w.hi) next_scales<FMT, 2>(st, w, w.lo, scratch);
+    __syncthreads();
     bool tiny = false;
     for (int i = 0; i < p.T; ++i) tiny |= is_tiny(wk.xmax[i]);
     // columns past T repeat the last token and are never stored
@@ -1004,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     __syncthreads();
     // one maximum per pair and CTA: thousands of them on a few lines delayed the barrier by 6 us
-    if (tid < p.T * p.k && wk.htop[tid] != 0u) atomicMax(hmax + tid, wk.htop[tid]);
+    if (tid < p.T * p.k && wk.htop[tid] != 0u) atomicMax(hmax + kHmaxStep * tid, wk.htop[tid]);
     grid_arrive(barrier + 1);
     // the weights do not wait for the other CTAs
     start_stream<FMT, 3>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
@@ -1013,23 +1023,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       if (blockIdx.x == 0 && tid == 0) p.sync[0] = 1u - parity;  // every CTA has read it
       const int pairs = p.T * p.k;  // <= 256
-      if (tid < pairs) {
-        const uint32_t top = __ldcg(hmax + tid);
-        wk.hscale[tid] = scale_up(top);
-        if (is_tiny(top)) wk.tiny = 1;
-      }
-      __syncthreads();
       // h to fp16: all of it into every CTA's shared memory, or, where that is
       // too small, each CTA a share in global memory and one more barrier
       const float4* src = reinterpret_cast<const float4*>(p.hbuf);
       const int chunks = pairs * nd2 * 16;  // of 8 values
       const bool here = (uint32_t)chunks * 16u <= plan.act;
-      for (int i = here ? tid : (int)(blockIdx.x * kThreads) + tid; i < chunks; i += here ? kThreads : (int)gridDim.x * kThreads) {
-        const float4 u = __ldcg(src + 2 * i), v = __ldcg(src + 2 * i + 1);
+      const int c0 = here ? tid : (int)(blockIdx.x * kThreads) + tid, cs = here ? kThreads : (int)gridDim.x * kThreads;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;  // the first chunk comes along with the maxima
+      if (c0 < chunks) u = __ldcg(src + 2 * c0), v = __ldcg(src + 2 * c0 + 1);
+      if (tid < pairs) {
+        const uint32_t top = __ldcg(hmax + kHmaxStep * tid);
+        wk.hscale[tid] = scale_up(top);
+        if (is_tiny(top)) wk.tiny = 1;
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int i = c0; i < chunks;) {
         const float sc = wk.hscale[i / (nd2 * 16)];
         __half2 q[4] = {__floats2half2_rn(u.x * sc, u.y * sc), __floats2half2_rn(u.z * sc, u.w * sc),
                         __floats2half2_rn(v.x * sc, v.y * sc), __floats2half2_rn(v.z * sc, v.w * sc)};
-        *(here ? reinterpret_cast<uint4*>(smem_raw) + i : p.h16 + i) = *reinterpret_cast<uint4*>(q);
+        const int to = i;
+        i += cs;
+        if (i < chunks) u = __ldcg(src + 2 * i), v = __ldcg(src + 2 * i + 1);
+        *(here ? reinterpret_cast<uint4*>(smem_raw) + to : p.h16 + to) = *reinterpret_cast<uint4*>(q);
       }
       if (here) {
         __syncthreads();
@@ -1096,7 +1112,7 @@ Plan make_plan(int fmt, int T, int H, int pairs, int I) {
 size_t moe_decode_workspace(int T, int k, int I, size_t* at) {
   size_t n = kSyncBytes;
   at[0] = n;  // hmax
-  n = align256(n + 2 * (size_t)kMaxPairs * sizeof(unsigned));
+  n = align256(n + 2 * (size_t)kMaxPairs * kHmaxStep * sizeof(unsigned));
   at[1] = n;  // unit_count
   n = align256(n + (size_t)(kMoeDecodeMaxTH / 32) * sizeof(unsigned));  // the same place for every shape: it stays zero
   at[2] = n;  // part
