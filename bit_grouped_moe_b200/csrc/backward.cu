@@ -133,10 +133,18 @@ __global__ void __launch_bounds__(kThreads) route_topk_backward_kernel(const int
 cudaError_t launch_combine_backward(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* s2f,
                                     const int32_t* f2s, const float* weights, int M, int k, int N,
                                     __nv_bfloat16* dy, float* d_weights, cudaStream_t stream) {
-  const int rpc = kWarps;  // rows per CTA
-  return launch_pdl(combine_backward_kernel<1>, dim3((unsigned)((M + rpc - 1LL) / rpc)), dim3(kThreads), 0, stream,
-                    reinterpret_cast<const uint4*>(dout), reinterpret_cast<const uint4*>(y), s2f, f2s, weights, M, k,
-                    N / 8, reinterpret_cast<uint4*>(dy), d_weights);
+  auto launch = [&](auto* kernel, int warps) {
+    const int rpc = kWarps / warps;  // rows per CTA
+    return launch_pdl(kernel, dim3((unsigned)((M + rpc - 1LL) / rpc)), dim3(kThreads), 0, stream,
+                      reinterpret_cast<const uint4*>(dout), reinterpret_cast<const uint4*>(y), s2f, f2s, weights, M, k,
+                      N / 8, reinterpret_cast<uint4*>(dy), d_weights);
+  };
+  switch (warps_per_row(M, N / 8)) {
+    case 8: return launch(combine_backward_kernel<8>, 8);
+    case 4: return launch(combine_backward_kernel<4>, 4);
+    case 2: return launch(combine_backward_kernel<2>, 2);
+    default: return launch(combine_backward_kernel<1>, 1);
+  }
 }
 
 cudaError_t launch_route_topk_backward(const int32_t* ids, const float* probs, const float* d_weights, int T, int k,

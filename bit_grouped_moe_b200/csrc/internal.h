@@ -164,6 +164,17 @@ cudaError_t launch_swiglu_ckpt8_backward(const __nv_bfloat16* dh, const uint8_t*
                                          const float* weights, int M, int I, __nv_bfloat16* d_gate_up,
                                          __nv_bfloat16* h, float* d_weights, cudaStream_t stream);
 
+// Warps per row (1, 2, 4, 8) of the row kernels of ckpt8.cu and backward.cu, whose lanes move 8 values each.  Many
+// rows fill the GPU with one warp each, which wastes no lane at a row's end and adds no block barrier (32768 rows of
+// 2048: 106 us, with 8 warps 139); few rows need more warps to have enough loads in flight (252 rows of 2880: 7.6 us
+// with one, 3.1 with four; 72 rows of 1024: 4.2 and 2.4 with eight).  More warps than a row has 256-value pieces
+// would idle.
+inline int warps_per_row(int rows, int octets) {
+  int w = 1;
+  while (w < 8 && (long long)rows * w * 2 <= 1184 && octets > 32 * w) w *= 2;
+  return w;
+}
+
 // backward.cu: backward of the combine (y null: d_weights null) and of the router epilogue
 cudaError_t launch_combine_backward(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* s2f,
                                     const int32_t* f2s, const float* weights, int M, int k, int N,
