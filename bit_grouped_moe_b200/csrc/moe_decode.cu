@@ -821,11 +821,16 @@ __device__ __forceinline__ void stage_x(const MoeDecodeArgs& p, Work& s, uint4* 
 #pragma unroll 4
     for (int i = first; i < H8; i += step) {
       const uint4 v = __ldg(x + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t q = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+      if (__vcmpgeu2(q, 0x7F807F80u) != 0u) {  // an infinity or a NaN stays out
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = w[j] & 0x7FFFu, b = (w[j] >> 16) & 0x7FFFu;
-        m = max(m, max(a >= 0x7F80u ? 0u : a, b >= 0x7F80u ? 0u : b));
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t a = (w[j >> 1] >> (16 * (j & 1))) & 0x7FFFu;
+          m = max(m, a >= 0x7F80u ? 0u : a);
+        }
+      } else {
+        m = max(m, max(q & 0xFFFFu, q >> 16));
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
@@ -886,11 +891,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned parity = __ldcg(p.sync) & 1u;
   unsigned* const barrier = p.sync + 1 + 3 * parity;
   unsigned* const hmax = p.hmax + kMaxPairs * kHmaxStep * parity;
-  // the table and x are laid out while the router's first weights arrive
+  // the table is laid out while the router's first weights arrive, x while the CTAs meet
   const RouterPart part(p, tid);
   __syncthreads();
   if (FMT == 0) build_table(reinterpret_cast<uint32_t*>(smem_raw + plan.table), tid);
-  stage_x<FMT>(p, wk, xs, tid);
   if (p.router_w != nullptr) {
     if (p.T == 1) router_product<1>(p, wk, part, tid);
     else if (p.T == 2) router_product<2>(p, wk, part, tid);
@@ -898,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else router_product<8>(p, wk, part, tid);
     grid_arrive(barrier);
   }
+  stage_x<FMT>(p, wk, xs, tid);
   const int nd2 = (p.I + kDK - 1) / kDK;
   if (p.I % kDK != 0) {  // the last item of every row of h: zero past I
     const int pad = (nd2 * kDK - p.I) / 8;  // chunks
