@@ -275,3 +275,15 @@ def test_no_tokens(g):
     torch.cuda.synchronize()
     s = g.call_stats_get("gnf4_moe_decode_nf4")
     assert (s["calls"], s["engaged"], s["rows"]) == (2, 1, 2)
+
+
+def test_short_or_misaligned_workspace_is_refused_before_any_launch(g):
+    lay = Layer(g, "mxfp4", 2, 4, 2, 64, 64, seed=91)
+    lay.out.fill_(7.0)
+    for ws in (lay.ws[:-1], lay.ws[:0], torch.zeros(lay.ws.numel() + 8, dtype=torch.uint8, device="cuda")[8:]):
+        lay.ws = ws
+        with pytest.raises(g.Gnf4Error) as e:
+            lay.call()
+        assert e.value.status == g.ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.all(lay.out == 7.0)
