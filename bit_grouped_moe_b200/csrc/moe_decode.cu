@@ -83,7 +83,6 @@ struct Work {
   float red[kWarps][kMaxT];     // router products per warp
   uint32_t xmax[kMaxT];         // largest finite |x| of a token (fp32 bits)
   float hscale[kMaxPairs];      // scale of a pair's fp16 h
-  uint32_t htop[kMaxPairs];     // largest finite |h| of a pair in this CTA (fp32 bits)
   int nhit;
   int tiny;                     // a pair's h lies below 2^kTinyExp throughout
   int ok;
@@ -98,8 +97,8 @@ __device__ __forceinline__ float scale_up(uint32_t top) { return __uint_as_float
 __device__ __forceinline__ float scale_down(uint32_t top) { return __uint_as_float((exp_field(top) - 14u) << 23); }
 __device__ __forceinline__ bool is_tiny(uint32_t top) { return top != 0u && top < (uint32_t)(127 + kTinyExp) << 23; }
 
-// Offsets in the dynamic shared window.  x in fragment order (in phase 3: 64
-// bytes of h per lane), Route, Work and MXFP4's scale scratch first; NF4's pair table at a 64 KB boundary (0x10000, or
+// Offsets in the dynamic shared window.  x in fragment order (in phase 3: h,
+// where there is room), Route, Work and MXFP4's scale scratch first; NF4's pair table at a 64 KB boundary (0x10000, or
 // 0x20000 where x needs the room); then the rings.
 struct Plan {
   uint32_t route, work, scratch, table, ring, total;
@@ -115,12 +114,11 @@ template <int FMT>
 __device__ __forceinline__ constexpr int scratch_row(int r) {
   return FMT == 0 ? (r >> 4) * 256 + (r & 15) * 8 : 16 * r;
 }
-constexpr uint32_t kHBytes = kThreads * 64;  // phase 3: h of one item
 // Workspace words: [0] parity of the call, [1 + b + 3 * parity] arrivals at grid barrier b.  A call uses the counters
 // (and the hmax) of its parity and zeroes the other ones, which the call before it used; no CTA has to wait for the
 // others to leave.
 constexpr int kSyncBytes = 256;
-constexpr int kHmaxStep = 32;  // words: a line for every pair's maximum, so that the CTAs' updates do not queue
+constexpr int kHmaxStep = 32;  // words: a line for every pair's maximum, so that the warps' updates do not queue (6 us at T = 8)
 
 // NF4 pairs as fp16, one copy per lane, 256 bytes per entry.
 __device__ __forceinline__ void build_table(uint32_t* lut, int tid) {
@@ -196,6 +194,7 @@ __device__ __forceinline__ bool grid_wait(unsigned* ctr, unsigned* err, int* ok)
       unsigned v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
       if (v >= gridDim.x) break;
+      __nanosleep(40);  // 148 pollers on one line delay the arrivals (4% of a T = 8 call)
       if (clock64() - t0 > kSpinLimitCycles) {
         atomicOr(err, GNF4_DEVERR_TIMEOUT);
         good = 0;
@@ -470,18 +469,20 @@ __device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&d)[4],
   for (int i = 0; i < 4; ++i) acc[i] = fmaf(i < 2 ? sa : sb, TINY ? d[i] * unit[i & 1] : d[i], acc[i]);
 }
 
-// acc[tile] += the item's weights (shared memory) times the lane's activations: chunk c at x + c * x_step.
+// acc[tile] += the item's weights (shared memory) times the lane's activations: chunk c at x + c * x_step in shared
+// memory (HERE), else own[c].
 // Tile k holds item rows r0 + 8 STEP_T k (its first 8) and 8 STEP_H further.
-template <int FMT, bool TINY, int STEP_T, int STEP_H>
+template <int FMT, bool TINY, bool HERE, int STEP_T, int STEP_H>
 __device__ __forceinline__ void multiply(float (&acc)[2][4], uint32_t item, uint32_t scratch, uint32_t x,
-                                         uint32_t x_step, const float (&unit)[2], int r0, int t, uint32_t lanesel) {
+                                         uint32_t x_step, const uint4 (&own)[4], const float (&unit)[2], int r0, int t,
+                                         uint32_t lanesel) {
+  uint4 v[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) v[b] = HERE ? lds_u128(x + b * x_step) : own[b];
   const uint32_t key = (uint32_t)(r0 >> 1) & 3u;  // the box's 64-byte swizzle: 16-byte chunk ^= (row / 2) % 4
   if (FMT == 1) {
     const uint32_t at = item + 64 * r0 + 4 * t + (key << 4);
     scratch += 16 * r0;
-    uint4 v[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) v[b] = lds_u128(x + b * x_step);
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       const int ra = 8 * STEP_T * tile, rb = ra + 8 * STEP_H;
@@ -506,7 +507,7 @@ __device__ __forceinline__ void multiply(float (&acc)[2][4], uint32_t item, uint
 #pragma unroll
     for (int b = 0; b < 2; ++b) {  // one 64-block: 16 codes of each row
       const uint32_t q = at + (((uint32_t)(2 * b + (t >> 1)) ^ key) << 4);
-      const uint4 v0 = lds_u128(x + 2 * b * x_step), v1 = lds_u128(x + (2 * b + 1) * x_step);
+      const uint4 v0 = v[2 * b], v1 = v[2 * b + 1];
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile) {
         const int ra = 8 * STEP_T * tile, rb = ra + 8 * STEP_H;
@@ -605,18 +606,11 @@ struct Stream {
     const int r = s.row[ei][g];
     return r < 0 ? ~r : r;
   }
-  // Phase 3 with h in global memory: this lane's fp16 h of an item, and to its slot.
+  // Phase 3 with h in global memory: this lane's fp16 h of an item.
   __device__ __forceinline__ void load_h(uint4 (&h)[4], const Cursor& c) const {
     const uint4* q = p.h16 + ((size_t)pair(c.ei) * nd + c.d) * 16 + t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = __ldcg(q + 4 * i);
-  }
-  __device__ __forceinline__ void store_h(uint32_t slot, const uint4 (&h)[4]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(slot + 512 * i), "r"(h[i].x), "r"(h[i].y),
-                   "r"(h[i].z), "r"(h[i].w)
-                   : "memory");
   }
   // 1 / the scale of column q (0, 1) of this lane; 0 for a phase 3 column whose token did not choose expert ei.
   __device__ __forceinline__ float unit_of(int ei, int q) const {
@@ -711,8 +705,8 @@ __device__ __forceinline__ void next_scales(const Stream<FMT, PHASE>& st, Walk<F
 // phase 3: h holds the first item's activations.  `emit(unit, acc, whole)` is
 // called by one full warp per unit of the CTA's range, whole = all of its items
 // were here.  x: phase 2 this lane's x in shared memory (items 4 * x_step
-// apart); phase 3 this lane's column of h in shared memory (HERE), else its
-// slot for the h of one item.  A wait that gives up flags the timeout; the
+// apart); phase 3 this lane's column of h in shared memory (HERE), else h holds
+// the first item's.  A wait that gives up flags the timeout; the
 // stream then runs to its end on whatever the ring holds.
 template <int FMT, int PHASE, bool TINY, bool HERE, class Emit>
 __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, Work& wk,
@@ -722,7 +716,7 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
   auto split = [&](int i) { return a + (b - a) * i / kWarps; };
   // NF4 reads 8 bytes per lane: this order of the 8 rows keeps each half of the warp on 32 banks
   const int r0 = FMT == 0 ? (st.g & 1) | ((st.g & 2) << 1) | ((st.g & 4) >> 1) : st.g;
-  if (!HERE && lo < hi) st.store_h(x, h);
+  uint4 own[4] = {};  // !HERE: the present item's activations; h: the next one's
   uint32_t column = x;  // phase 3, HERE: the current expert's row of h
   if (PHASE == 3 && HERE && lo < hi) column = x + 256u * (uint32_t)(st.pair(w.cur.ei) * st.nd);
   float acc[2][4] = {};
@@ -735,18 +729,21 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
     const int unit = w.cur.unit, ei = w.cur.ei, d = w.cur.d;
     if ((d & 3) == 0 && item > lo) next_scales<FMT, PHASE>(st, w, item, scratch);
     const bool turn = st.advance(w.cur), more = item + 1 < hi;
-    if (!HERE && more) st.load_h(h, w.cur);
+    if (!HERE) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = h[i];
+      if (more) st.load_h(h, w.cur);
+    }
     if (PHASE == 3 && TINY) unit2[0] = st.unit_of(ei, 0), unit2[1] = st.unit_of(ei, 1);
     if (!mbar_try_wait(ring.full + ring.get, ring.parity))
       box_wait_slow(ring.full + ring.get, ring.parity, err, &wk.abort);
     __syncwarp();
-    multiply<FMT, TINY, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(
+    multiply<FMT, TINY, HERE, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(
         PHASE == 3 ? one : acc, ring.base + ring.get * kItemBytes, scratch + (d & 3) * kScratchItem,
-        HERE ? column + 4 * x_step * d : x, x_step, unit2, r0, st.t, lanesel);
+        column + 4 * x_step * d, x_step, own, unit2, r0, st.t, lanesel);
     ring.popped();
     __syncwarp();  // every lane has read the box and the scratch
     issue_box(st, ring, w);
-    if (!HERE && more) st.store_h(x, h);
     if (!turn && more) continue;
     if (PHASE == 3) {
       // columns of tokens that did not choose the expert are dropped, not
@@ -887,7 +884,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane < plan.stages) mbar_init(ring.full + lane, 1);
   fence_mbar_init();
-  if (tid < kMaxPairs) wk.htop[tid] = 0u;
   const unsigned parity = __ldcg(p.sync) & 1u;
   unsigned* const barrier = p.sync + 1 + 3 * parity;
   unsigned* const hmax = p.hmax + kMaxPairs * kHmaxStep * parity;
@@ -966,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (r >= 0 && g == 0) atomicMax(&wk.htop[r], top);
+        if (r >= 0 && g == 0) atomicMax(hmax + kHmaxStep * r, top);
       }
     };
     if (tiny)
@@ -1017,9 +1013,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       store(unit, sum, r0);
     };
-    __syncthreads();
-    // one maximum per pair and CTA: thousands of them on a few lines delayed the barrier by 6 us
-    if (tid < p.T * p.k && wk.htop[tid] != 0u) atomicMax(hmax + kHmaxStep * tid, wk.htop[tid]);
     grid_arrive(barrier + 1);
     // the weights do not wait for the other CTAs
     start_stream<FMT, 3>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
@@ -1064,11 +1057,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = grid_wait(barrier + 2, p.err, &wk.ok);
         if (ok) {
           if (w.lo < w.hi) st.load_h(h, w.cur);
-          const uint32_t slot = kWindow + (uint32_t)(warp * 2048 + lane * 16);
           if (wk.tiny)
-            run_stream<FMT, 3, true, false>(st, ring, w, wk, p.err, scratch, slot, 512u, lanesel, rings, warp, h, emit);
+            run_stream<FMT, 3, true, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
           else
-            run_stream<FMT, 3, false, false>(st, ring, w, wk, p.err, scratch, slot, 512u, lanesel, rings, warp, h, emit);
+            run_stream<FMT, 3, false, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
         }
       }
     }
@@ -1090,7 +1082,7 @@ Plan make_plan(int fmt, int T, int H, int pairs, int I) {
   // room for all of h where it is cheap: up to 64 KB without a larger x
   const uint32_t h = (uint32_t)pairs * (uint32_t)((I + kDK - 1) / kDK) * 256u;
   const uint32_t limit = fmt == 0 ? 32768u : 65536u;
-  q.act = x > kHBytes ? x : kHBytes;
+  q.act = x;
   if (h > q.act && h <= limit) q.act = h;
   q.route = q.act;
   q.work = up(q.route + (uint32_t)sizeof(Route), 16);
