@@ -31,7 +31,68 @@ namespace {
 constexpr int kThreads = 256;                                                     // forward
 constexpr int row_threads(int wpr) { return wpr == 8 ? 256 : 128; }               // backward (smaller CTAs: 4% faster)
 
-__device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// Two floats in a register pair, for the packed fp32 instructions: the forward
+// kernel is bound by issue before it is by memory (78% of the issue slots with
+// one value per instruction; 88.5 us for 32768 rows of 2048, 85.1 packed).  The
+// backward kernel has three outputs to hold: its pairs cost registers, and the
+// loads in flight with them (97 us instead of 92).
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+
+// 1 / (1 + 2^(-g log2 e)).  The two approximate instructions are within a few
+// units of 2^-23; 2^x overflows to infinity, whose reciprocal is 0: the limit.
+__device__ __forceinline__ float exp2_approx(float x) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid_f32(float g) { return rcp_approx(1.0f + exp2_approx(-kLog2e * g)); }
+__device__ __forceinline__ F2 sigmoid2(F2 g) {
+  const float2 e = split(mul2(g, both(-kLog2e)));
+  const float2 d = split(add2(pair(exp2_approx(e.x), exp2_approx(e.y)), both(1.0f)));
+  return pair(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, F2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t pack2(F2 f) {
+  const float2 p = split(f);
+  __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+  return *reinterpret_cast<uint32_t*>(&b);
+}
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+  return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -41,7 +102,6 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
-
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint32_t o[4];
 #pragma unroll
@@ -51,7 +111,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-
 __device__ __forceinline__ void decode8(uint2 c, float sc, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -63,7 +122,7 @@ __device__ __forceinline__ void decode8(uint2 c, float sc, float (&f)[8]) {
 
 // Eight consecutive values f (bf16 bits v) of a 32-block shared by lanes
 // 4i..4i+3: the codes, and the scale byte (the same in the four lanes).
-__device__ __forceinline__ uint2 quant8(uint4 v, const float (&f)[8], uint32_t* scale) {
+__device__ __forceinline__ uint2 quant8(uint4 v, const F2 (&f)[4], uint32_t* scale) {
   // |bf16| compares like its bits with the sign cleared
   uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
   m = max(m & 0xFFFFu, m >> 16);
@@ -86,13 +145,14 @@ __device__ __forceinline__ uint2 quant8(uint4 v, const float (&f)[8], uint32_t* 
   const float inv = __uint_as_float((uint32_t)(127 - X) << 23);  // 2^-X: 127 - X is in [7, 254]
   uint32_t out[2] = {0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    float a = f[i] * inv, b = f[i + 1] * inv;
+  for (int i = 0; i < 4; ++i) {
+    float2 a = split(mul2(f[i], both(inv)));
     if (wild) {  // the finite-saturating conversion would store an infinity as 448: inf - inf is NaN, 0 otherwise
-      a += f[i] - f[i];
-      b += f[i + 1] - f[i + 1];
+      const float2 b = split(f[i]);
+      a.x += b.x - b.x;
+      a.y += b.y - b.y;
     }
-    out[i >> 2] |= cvt_e4m3x2(b, a) << (8 * (i & 2));
+    out[i >> 1] |= cvt_e4m3x2(a.y, a.x) << (16 * (i & 1));
   }
   *scale = (uint32_t)(X + 127);
   return make_uint2(out[0], out[1]);
@@ -104,8 +164,8 @@ __device__ __forceinline__ int live_rows(const int* num_rows, int M) {
 
 // One thread, PER times: 8 gate values, the 8 matching up values, 8 outputs.
 // All loads of a thread are issued before the first is used.  32768 rows of
-// 2048: 97.6 us with PER = 1, 88.3 with 4 (6.1 TB/s); 72 rows of 1024: 2.0 and
-// 3.6 us, so few values take 1.
+// 2048: 85 us (6.4 TB/s) with PER = 4, 9 us more with 1; 72 rows of 1024: 2.0
+// us with 1, 3.6 with 4, so few values take 1.
 template <typename Idx, int PER>
 __global__ void __launch_bounds__(kThreads) swiglu_ckpt8_kernel(const __nv_bfloat16* __restrict__ gate_up, int M,
                                                                 int I8, const int* __restrict__ num_rows,
@@ -133,14 +193,14 @@ __global__ void __launch_bounds__(kThreads) swiglu_ckpt8_kernel(const __nv_bfloa
   }
 #pragma unroll
   for (int n = 0; n < PER; ++n) {
-    float g[8], u[8];
+    F2 g[4], u[4];
     unpack8(gv[n], g);
     unpack8(uv[n], u);
     uint32_t gs, us;
     const uint2 gc = quant8(gv[n], g, &gs), uc = quant8(uv[n], u, &us);
     if (c[n] < 0) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = silu_mul(g[i], u[i]);
+    for (int i = 0; i < 4; ++i) g[i] = mul2(mul2(g[i], sigmoid2(g[i])), u[i]);
     h[(at[n] + c[n]) >> 1] = pack8(g);  // at = 2 I8 row + c, h lies at I8 row + c
     codes[at[n]] = gc;
     codes[at[n] + I8] = uc;
@@ -153,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_ckpt8_kernel(const __nv_bfloa
 
 // WPR warps per row, a lane's next 16 values fetched while it works on the
 // present ones; the row's dot product is added lane by lane, then by shuffles,
-// then warp by warp.  32768 rows of 2048 in 97 us (5.6 TB/s; without the early
+// then warp by warp.  32768 rows of 2048 in 92 us (5.9 TB/s; without the early
 // fetch and with 59 registers per thread 106 us).
 template <int WPR>
 __global__ void __launch_bounds__(row_threads(WPR), 1280 / row_threads(WPR)) swiglu_ckpt8_backward_kernel(
