@@ -166,8 +166,8 @@ cudaError_t launch_swiglu_ckpt8_backward(const __nv_bfloat16* dh, const uint8_t*
 
 // Warps per row (1, 2, 4, 8) of the row kernels of ckpt8.cu and backward.cu, whose lanes move 8 values each.  Many
 // rows fill the GPU with one warp each, which wastes no lane at a row's end and adds no block barrier (32768 rows of
-// 2048: 106 us, with 8 warps 139); few rows need more warps to have enough loads in flight (252 rows of 2880: 7.6 us
-// with one, 3.1 with four; 72 rows of 1024: 4.2 and 2.4 with eight).  More warps than a row has 256-value pieces
+// 2048: 92 us, with 8 warps 139); few rows need more warps to have enough loads in flight (252 rows of 2880: 7.6 us
+// with one, 3.1 with four; 72 rows of 1024: 3.2 and 2.3).  More warps than a row has 256-value pieces
 // would idle.
 inline int warps_per_row(int rows, int octets) {
   int w = 1;

@@ -44,13 +44,19 @@
 //   Phase 2: the MMA's 8 columns are the T tokens, whichever expert they
 // chose; products of tokens that did not choose it are computed (the MMA has
 // the columns anyway) and dropped.  x lies in shared memory in fragment order.
-//   Phase 3: columns as in phase 2; a lane fetches its part of h for the next
-// item while it works on this one.
+//   Phase 3: columns as in phase 2; h lies in shared memory where there is room,
+// else a lane fetches its part for the next item while it works on this one.
 //
 // Decode: MXFP4 converts a byte to an fp16 pair with one instruction
 // (cvt.rn.f16x2.e2m1x2: half a cycle per SM, measured).  NF4 looks a byte up in
 // the per-lane pair table of the grouped GEMV (one PRMT and one shared load).
 // Rounded to 16 bits apart from that: out, once.
+//
+// Bound: 18 to 23 us of a call are latency (three meetings of the grid, two
+// pipeline starts, the cross-CTA tail).  In the loops MXFP4 is bound by HBM
+// (5.6-5.9 TB/s; the loads alone 6.6), NF4 by shared memory (122 cycles per
+// item, of which 64 are lookups: 5.3 TB/s; measured 4.2).  Calls: OLMoE shape
+// T = 1 26 us, T = 8 68 us; 7168 / 2048, 48 experts, T = 8, MXFP4 184 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1079,7 +1085,10 @@ Plan make_plan(int fmt, int T, int H, int pairs, int I) {
   Plan q{};
   auto up = [](uint32_t n, uint32_t a) { return (n + a - 1) / a * a; };
   const uint32_t x = (uint32_t)((H + kDK - 1) / kDK) * 256u * (uint32_t)T;
-  // room for all of h where it is cheap: up to 64 KB without a larger x
+  // Room for all of h where that is cheaper than sharing the conversion and meeting once more.  MXFP4: 23 KB (T = 1,
+  // k = 4, I = 2880) 32.5 us instead of 34.5, 64 KB (T = 4, k = 8, I = 1024) 39.9 instead of 40.6, but 128 KB 56.9
+  // instead of 53.0.  NF4: 32 KB 33.8 instead of 34.5, but 64 KB, which moves the table, 48.2 instead of 47.4.  An x
+  // that is larger leaves the room anyway.
   const uint32_t h = (uint32_t)pairs * (uint32_t)((I + kDK - 1) / kDK) * 256u;
   const uint32_t limit = fmt == 0 ? 32768u : 65536u;
   q.act = x;
@@ -1125,11 +1134,12 @@ static cudaError_t launch_t(const CUtensorMap& map1, const CUtensorMap& map2, co
                             cudaStream_t stream) {
   static std::atomic<bool> configured[64];
   const Plan plan = make_plan(FMT, p.T, p.H, p.T * p.k, p.I);
-  if (plan.stages < 1) return cudaErrorInvalidConfiguration;
+  const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
+  if (plan.stages < 1 || p.E > 8 * grid) return cudaErrorInvalidConfiguration;  // the router: 8 experts a CTA
   cudaError_t e = set_smem_limit_once(moe_decode_kernel<FMT>, (int)kMaxWindow, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(num_sms < kMaxGrid ? num_sms : kMaxGrid));
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = plan.total;
   cfg.stream = stream;

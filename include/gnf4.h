@@ -514,10 +514,12 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
  *     h[t, j]  = silu(G_e x[t]) * (U_e x[t]),  e = topk_ids[t, j], G_e / U_e
  *       rows [0, I) / [I, 2I) of w_gate_up[e],
  *     out[t]   = sum_j topk_weights[t, j] * (D_e h[t, j]),  D_e = w_down[e].
- * Sums are fp32.  Rounded to bf16: topk_weights[t, j] * h[t, j], out, and the
- * 16 NF4 codes (after a scaling that minimises their error; absmax is applied
- * in fp32); MXFP4 weights are exact.  Two calls with the same inputs give the
- * same bits.
+ * Sums and scales are fp32, out is rounded once to bf16.  The products run on
+ * fp16 values that a power of two brings into range: x (scaled by the token's
+ * largest; its bf16 values are exact down to 2^-28 of that, and within 2^-39
+ * of it below), topk_weights[t, j] * h[t, j] (scaled by the
+ * pair's largest; rounded to 11 bits), the NF4 codes (within 2^-12) and the
+ * MXFP4 codes (exact).  Two calls with the same inputs give the same bits.
  *   x             bf16 [T, H];
  *   router_w      bf16 [E, H], or NULL: logits are then an input;
  *   bias          fp32 [E] or NULL: added for the selection only;
@@ -535,6 +537,7 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
  *                 device error zero it again.  Calls
  *                 that may overlap on the GPU (two streams, two graphs) need a
  *                 workspace each.
+ * Outputs and workspace may not overlap inputs.
  * Rules: 0 <= T <= 8, 1 <= E <= 1024, 1 <= k <= min(E, 32), H and I multiples
  * of 64 (NF4) or 32 (MXFP4), H >= that, T*H <= 57344 and H <= 57344,
  * that <= I <= 65536.  x, router_w, w_gate_up, w_down, out and workspace
@@ -581,6 +584,8 @@ gnf4_status gnf4_moe_decode_mxfp4(const void *x, const void *router_w, const flo
  *   or NULL (= M; offsets + E of the routing is what a sorted batch passes):
  *   rows at and past it are neither read nor written; h bf16 [M, I] OUT; codes uint8
  *   [M, 2I] OUT; scales uint8 [M, 2I/32] OUT.
+ * A sigmoid below 2^-126 (a gate below -87.3) counts as 0, here and in the
+ * backward.  Outputs may not overlap inputs.
  * Rules: M >= 0, I >= 32 and I % 32 == 0, M*I <= 2^40; gate_up, h and codes
  * 16-byte aligned. */
 gnf4_status gnf4_swiglu_ckpt8(const void *gate_up, int M, int I, const int32_t *num_rows, void *h, uint8_t *codes,
@@ -619,6 +624,7 @@ gnf4_status gnf4_swiglu_ckpt8_backward(const void *dh, const uint8_t *codes, con
  *   sorted_to_flat int32 [T*k]; flat_to_sorted int32 [T*k] or NULL (needed with
  *   d_weights); weights fp32 [T, k] or NULL; dy bf16 [T*k, N] OUT; d_weights
  *   fp32 [T, k] OUT or NULL.
+ * Outputs may not overlap inputs.
  * Rules: T >= 0, k >= 1, T*k < 2^31, N >= 8 and N % 8 == 0; dout, y and dy
  * 16-byte aligned. */
 gnf4_status gnf4_combine_backward(const void *dout, const void *y, const int32_t *sorted_to_flat,
