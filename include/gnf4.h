@@ -623,7 +623,7 @@ gnf4_status gnf4_swiglu_ckpt8_backward(const void *dh, const uint8_t *codes, con
  *   dout bf16 [T, N]; y bf16 [T*k, N] or NULL (needed with d_weights);
  *   sorted_to_flat int32 [T*k]; flat_to_sorted int32 [T*k] or NULL (needed with
  *   d_weights); weights fp32 [T, k] or NULL; dy bf16 [T*k, N] OUT; d_weights
- *   fp32 [T, k] OUT or NULL.
+ *   fp32 [T, k] OUT or NULL.  The two permutations are inverse to each other.
  * Outputs may not overlap inputs.
  * Rules: T >= 0, k >= 1, T*k < 2^31, N >= 8 and N % 8 == 0; dout, y and dy
  * 16-byte aligned. */
