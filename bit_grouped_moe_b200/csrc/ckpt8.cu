@@ -33,7 +33,7 @@ constexpr int row_threads(int wpr) { return wpr == 8 ? 256 : 128; }             
 
 // Two floats in a register pair, for the packed fp32 instructions: the forward
 // kernel is bound by issue before it is by memory (78% of the issue slots with
-// one value per instruction; 88.5 us for 32768 rows of 2048, 85.1 packed).  The
+// one value per instruction; 89 us for 32768 rows of 2048, 86 packed).  The
 // backward kernel has three outputs to hold: its pairs cost registers, and the
 // loads in flight with them (97 us instead of 92).
 struct F2 {
@@ -59,12 +59,18 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 __device__ __forceinline__ F2 both(float a) { return pair(a, a); }
 
-// 1 / (1 + 2^(-g log2 e)).  The two approximate instructions are within a few
-// units of 2^-23; 2^x overflows to infinity, whose reciprocal is 0: the limit.
-// Results below 2^-126 (g < -87.3) are flushed to 0 as well: silu(g) * u is off
-// by at most 2^-119 |u| there.
+// s = 1 / (1 + 2^(-g log2 e)), computed as 4 s = 1 / (1/4 + 2^(-g log2 e - 2)):
+// the approximate reciprocal flushes results below 2^-126, which this moves to
+// where 1 + e^-g overflows in fp32 anyway (g < -88.7: s = 0).  The approximate
+// instructions are within a few units of 2^-23, the exponent's rounding adds
+// (1 + |g|) 2^-23 at most: below a bf16 step even at g = -88.
 __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
   return x;
@@ -74,10 +80,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return x;
 }
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float sigmoid_f32(float g) { return rcp_approx(1.0f + exp2_approx(-kLog2e * g)); }
-__device__ __forceinline__ F2 sigmoid2(F2 g) {
-  const float2 e = split(mul2(g, both(-kLog2e)));
-  const float2 d = split(add2(pair(exp2_approx(e.x), exp2_approx(e.y)), both(1.0f)));
+__device__ __forceinline__ float sigmoid_f32(float g) {
+  return 0.25f * rcp_approx(0.25f + exp2_approx(fmaf(-kLog2e, g, -2.0f)));
+}
+__device__ __forceinline__ F2 sigmoid2_times4(F2 g) {
+  const float2 e = split(fma2(g, both(-kLog2e), both(-2.0f)));
+  const float2 d = split(add2(pair(exp2_approx(e.x), exp2_approx(e.y)), both(0.25f)));
   return pair(rcp_approx(d.x), rcp_approx(d.y));
 }
 
@@ -166,7 +174,7 @@ __device__ __forceinline__ int live_rows(const int* num_rows, int M) {
 
 // One thread, PER times: 8 gate values, the 8 matching up values, 8 outputs.
 // All loads of a thread are issued before the first is used.  32768 rows of
-// 2048: 85 us (6.4 TB/s) with PER = 4, 9 us more with 1; 72 rows of 1024: 2.0
+// 2048: 86 us (6.3 TB/s) with PER = 4, 9 us more with 1; 72 rows of 1024: 2.0
 // us with 1, 3.6 with 4, so few values take 1.
 template <typename Idx, int PER>
 __global__ void __launch_bounds__(kThreads) swiglu_ckpt8_kernel(const __nv_bfloat16* __restrict__ gate_up, int M,
@@ -202,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_ckpt8_kernel(const __nv_bfloa
     const uint2 gc = quant8(gv[n], g, &gs), uc = quant8(uv[n], u, &us);
     if (c[n] < 0) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = mul2(mul2(g[i], sigmoid2(g[i])), u[i]);
+    for (int i = 0; i < 4; ++i) g[i] = mul2(mul2(mul2(g[i], both(0.25f)), sigmoid2_times4(g[i])), u[i]);
     h[(at[n] + c[n]) >> 1] = pack8(g);  // at = 2 I8 row + c, h lies at I8 row + c
     codes[at[n]] = gc;
     codes[at[n] + I8] = uc;

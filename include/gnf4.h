@@ -584,8 +584,8 @@ gnf4_status gnf4_moe_decode_mxfp4(const void *x, const void *router_w, const flo
  *   or NULL (= M; offsets + E of the routing is what a sorted batch passes):
  *   rows at and past it are neither read nor written; h bf16 [M, I] OUT; codes uint8
  *   [M, 2I] OUT; scales uint8 [M, 2I/32] OUT.
- * A sigmoid below 2^-126 (a gate below -87.3) counts as 0, here and in the
- * backward.  Outputs may not overlap inputs.
+ * Where e^-gate overflows fp32 (a gate below -88.7) the sigmoid counts as 0,
+ * here and in the backward.  Outputs may not overlap inputs.
  * Rules: M >= 0, I >= 32 and I % 32 == 0, M*I <= 2^40; gate_up, h and codes
  * 16-byte aligned. */
 gnf4_status gnf4_swiglu_ckpt8(const void *gate_up, int M, int I, const int32_t *num_rows, void *h, uint8_t *codes,

@@ -287,3 +287,23 @@ def test_short_or_misaligned_workspace_is_refused_before_any_launch(g):
         assert e.value.status == g.ERR_INVALID_ARG
     torch.cuda.synchronize()
     assert torch.all(lay.out == 7.0)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nf4"])
+def test_the_last_experts_of_stacks_past_4_gb(g, fmt):
+    """Experts placed at the end of stacks of 5.6 and 2.8 GB give the bits that the same experts give in a small stack."""
+    T, few, E, k, H, I = 3, 6, 384, 4, 7168, 2048
+    lay = Layer(g, fmt, T, few, k, H, I, router=False, seed=101)
+    lay.call()
+    want = lay.result()
+    for n in ("w1", "s1", "w2", "s2"):
+        part = lay.d[n]
+        lay.d[n] = torch.zeros((E,) + part.shape[1:], dtype=part.dtype, device="cuda")
+        lay.d[n][E - few:] = part
+    small = lay.logits
+    lay.logits = torch.full((T, E), -1e30, device="cuda")
+    lay.logits[:, E - few:] = small
+    lay.call()
+    out, ids, p, _ = lay.result()
+    assert torch.equal(ids, want[1] + (E - few)) and same_bits(p, want[2])
+    assert same_bits(out, want[0])

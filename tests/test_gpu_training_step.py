@@ -62,7 +62,7 @@ def run_forward(g, gu, I, num_rows=None):
     return h, codes, scales
 
 
-def check_forward(gu, I, h, codes, scales):
+def check_forward(gu, I, h, codes, scales, slack=0.0):
     v = ref.f64(gu)
     q, sc = ref.ckpt8(v)
     assert np.array_equal(scales.cpu().numpy(), sc), "scale bytes"
@@ -76,7 +76,7 @@ def check_forward(gu, I, h, codes, scales):
     assert np.all(got[big] == np.copysign(np.inf, want[big]))
     ok = np.isfinite(want) & (np.abs(want) < 2.0 ** 128 * (1 - 2.0 ** -9) * (1 - 2.0 ** -20))
     # one rounding to bf16, and exp, division, two products in fp32 (within 2^-20 together); below fp32's normal range absolutely
-    assert np.all(np.abs(got - want)[ok] <= (U + 2.0 ** -20) * np.abs(want)[ok] + 2.0 ** -126)
+    assert np.all(np.abs(got - want)[ok] <= (U + 2.0 ** -20 + slack) * np.abs(want)[ok] + 2.0 ** -126)
 
 
 @pytest.mark.parametrize("M,I", [(1, 32), (3, 96), (7, 160), (1, 2880), (33, 768), (260, 1024), (5, 65536)])
@@ -99,6 +99,17 @@ def test_forward_blocks_of_every_size_and_zero(g):
     check_forward(gu, I, *run_forward(g, gu, I))
 
 
+def test_forward_at_gates_whose_sigmoid_is_barely_normal(g):
+    """silu(g) u with s between 2^-128 and 2^-120 and an u that brings the product back to ordinary size."""
+    I = 32
+    a = np.ones((8, 2 * I))
+    a[:, :I] = -88.5 + np.arange(8 * I).reshape(8, I) * 0.02
+    a[:, I:] = 2.0 ** 100
+    gu = bf(a)
+    # the exponent -g log2 e < 128 is rounded by up to 2^-18, its constant by 2^-25 relatively: 2^-17 ln 2 in the result
+    check_forward(gu, I, *run_forward(g, gu, I), slack=2.0 ** -17)
+
+
 def test_forward_non_finite_values_spare_their_block(g):
     M, I = 2, 64
     a = inputs.rng(4).standard_normal((M, 2 * I))
@@ -119,6 +130,37 @@ def test_forward_rows_past_num_rows_are_left_alone(g, n):
     assert torch.all(h[live:] == 7.0) and torch.all(codes[live:] == 99) and torch.all(scales[live:] == 98)
     if live:
         check_forward(gu[:live], I, h[:live], codes[:live], scales[:live])
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_forward_and_backward_past_4_gb(g, wide):
+    """A small batch repeated until gate_up and d_gate_up pass 4 GB: every repetition has the small batch's bits.  wide:
+    M so large that octets need 64-bit indices, with the live rows at the front (the others are not touched)."""
+    rows, I = 96, 2048
+    gu = bf(inputs.rng(77).standard_normal((rows, 2 * I)))
+    dh = bf(inputs.rng(78).standard_normal((rows, I)))
+    small = run_forward(g, gu, I)
+    dsmall = torch.empty(rows, 2 * I, dtype=torch.bfloat16, device="cuda")
+    g.swiglu_ckpt8_backward(dh.cuda(), small[1], small[2], dsmall)
+    n = 3 if wide else 6000  # 6000 * 96 * 4096 * 2 = 4.7e9 bytes
+    M = 1 << 23 if wide else n * rows  # 2^23 * 256 octets = 2^31
+    tall = lambda t: t.as_strided((M, t.shape[1]), (0, 1)) if wide else t
+    nr = torch.tensor([n * rows], dtype=torch.int32, device="cuda") if wide else None
+    big = gu.cuda().repeat(n, 1)
+    h = torch.full((n * rows + 1, I), 7.0, dtype=torch.bfloat16, device="cuda")
+    codes = torch.full((n * rows + 1, 2 * I), 99, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n * rows + 1, 2 * I // 32), 98, dtype=torch.uint8, device="cuda")
+    cut = lambda t: t if wide else t[:-1]
+    g.swiglu_ckpt8(big, tall(cut(h)), codes, scales, num_rows=nr)
+    same_rows = lambda t, s: bool((t[:-1].view(n, rows, -1) == s).all())
+    assert same_rows(h.view(torch.int16), small[0].view(torch.int16))
+    assert same_rows(codes, small[1]) and same_rows(scales, small[2])
+    assert torch.all(h[-1] == 7.0) and torch.all(codes[-1] == 99) and torch.all(scales[-1] == 98)
+    del big, h
+    dbig = dh.cuda().repeat(n, 1)
+    d = torch.full((n * rows + 1, 2 * I), 7.0, dtype=torch.bfloat16, device="cuda")
+    g.swiglu_ckpt8_backward(tall(dbig), codes, scales, d, num_rows=nr)
+    assert same_rows(d.view(torch.int16), dsmall.view(torch.int16)) and torch.all(d[-1] == 7.0)
 
 
 # ------------------------------------------------------------------------------------------------ backward
