@@ -21,6 +21,7 @@
 // All arithmetic is fp32 on decoded values; h and the gradients are rounded
 // once to bf16, sums stay fp32 and are added in a fixed order.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -30,6 +31,18 @@ namespace {
 
 constexpr int kThreads = 256;                                                     // forward
 constexpr int row_threads(int wpr) { return wpr == 8 ? 256 : 128; }               // backward (smaller CTAs: 4% faster)
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
+  uint16_t pr;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pr) : "f"(hi), "f"(lo));
+  return pr;
+}
+// e4m3 pair (low byte = first element) -> two floats, exactly (through f16).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t pr) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pr));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
 
 // Two floats in a register pair, for the packed fp32 instructions: the forward
 // kernel is bound by issue before it is by memory (78% of the issue slots with

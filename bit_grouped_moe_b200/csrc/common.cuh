@@ -9,7 +9,6 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -142,24 +141,6 @@ __device__ __forceinline__ float silu_mul_tanh(float g, float u) {
   asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(hg));
   return fmaf(hg, t, hg) * u;
 }
-
-// ---------------------------------------------------------------- e4m3
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
-  uint16_t pr;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pr) : "f"(hi), "f"(lo));
-  return pr;
-}
-
-// e4m3 pair (low byte = first element) -> two floats, exactly (through f16).
-__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t pr) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pr));
-  const __half2 hh = *reinterpret_cast<const __half2*>(&h);
-  return __half22float2(hh);
-}
-
-// Exact power of two 2^e for e in [-126, 127].
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // ---------------------------------------------------------------- stream order
 // Programmatic dependent launch: let the next kernel of the stream be
@@ -310,15 +291,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
       "[%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
 

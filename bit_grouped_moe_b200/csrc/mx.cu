@@ -63,6 +63,23 @@ namespace {
 
 constexpr int kQThreads = 256;
 
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
+  uint16_t pr;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pr) : "f"(hi), "f"(lo));
+  return pr;
+}
+
+// e4m3 pair (low byte = first element) -> two floats, exactly (through f16).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t pr) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pr));
+  const __half2 hh = *reinterpret_cast<const __half2*>(&h);
+  return __half22float2(hh);
+}
+
+// Exact power of two 2^e for e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // floor(log2(a)) of a positive float given by its bits (subnormals included).
 __device__ __forceinline__ int ilog2_f32(uint32_t b) {
   return (b >> 23) != 0 ? (int)(b >> 23) - 127 : (31 - __clz((int)b)) - 149;
