@@ -653,9 +653,21 @@ struct Ring {
   }
 };
 
-// Waits for a box; the rare second look is kept out of the loop.
-__device__ __noinline__ void box_wait_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
-  mbar_wait(bar, parity, err, abort);
+// The second look at a box, by the whole warp: kept out of the loop.  False, in all lanes, if it gives up: *abort is
+// set then.
+__device__ __noinline__ bool box_wait_slow(uint64_t* bar, uint32_t parity, unsigned* err, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort)) != 0;
+}
+
+// The `n` boxes that the warp has issued and not read land (or a bounded wait each runs out).
+__device__ __noinline__ void drain_boxes(uint64_t* full, int stages, int get, uint32_t parity, int n) {
+  for (int i = 0; i < n; ++i) {
+    mbar_drain(full + get, parity);
+    if (++get == stages) {
+      get = 0;
+      parity ^= 1u;
+    }
+  }
 }
 
 // A warp's way through its items [lo, hi) of the CTA's [a, b).
@@ -721,10 +733,12 @@ __device__ __forceinline__ void next_scales(const Stream<FMT, PHASE>& st, Walk<F
 // called by one full warp per unit of the CTA's range, whole = all of its items
 // were here.  x: phase 2 this lane's x in shared memory (items 4 * x_step
 // apart); phase 3 this lane's column of h in shared memory (HERE), else h holds
-// the first item's.  A wait that gives up flags the timeout; the
-// stream then runs to its end on whatever the ring holds.
+// the first item's.  A wait that gives up flags the timeout and sets
+// wk.abort, which ends every warp's items at its next wait: a slot whose box
+// may be in flight is neither read nor issued again.  Returns false then, in
+// all threads, with no box of the CTA in flight.
 template <int FMT, int PHASE, bool TINY, bool HERE, class Emit>
-__device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, Work& wk,
+__device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, Work& wk,
                                            unsigned* err, uint32_t scratch, uint32_t x, uint32_t x_step,
                                            uint32_t lanesel, uint8_t* rings, int warp, uint4 (&h)[4], Emit emit) {
   const int a = w.a, b = w.b, lo = w.lo, hi = w.hi, per = st.per, lane = st.lane;
@@ -750,8 +764,11 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
       if (more) st.load_h(h, w.cur);
     }
     if (PHASE == 3 && TINY) unit2[0] = st.unit_of(ei, 0), unit2[1] = st.unit_of(ei, 1);
-    if (!mbar_try_wait(ring.full + ring.get, ring.parity))
-      box_wait_slow(ring.full + ring.get, ring.parity, err, &wk.abort);
+    if (!__all_sync(0xffffffffu, mbar_try_wait(ring.full + ring.get, ring.parity)) &&
+        !box_wait_slow(ring.full + ring.get, ring.parity, err, &wk.abort)) {
+      drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - item);
+      break;
+    }
     __syncwarp();
     multiply<FMT, TINY, HERE, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(
         PHASE == 3 ? one : acc, ring.base + ring.get * kItemBytes, scratch + (d & 3) * kScratchItem,
@@ -796,6 +813,7 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
 #pragma unroll
   for (int k = 0; k < 2; ++k) part(warp)[32 * k] = make_float4(head[k][0], head[k][1], head[k][2], head[k][3]);
   __syncthreads();
+  if (wk.abort) return false;
   if (tail) {  // add the parts of the warps after this one
     const int unit = (hi - 1) / per;
     const int first = max(unit * per, a), last = min((unit + 1) * per, b);
@@ -818,6 +836,7 @@ __device__ __forceinline__ void run_stream(const Stream<FMT, PHASE>& st, Ring& r
     }
     emit(unit, acc, last - first == per, r0, unit2);
   }
+  return true;
 }
 
 // x as fp16 scaled per token, in fragment order, zero past H.  All threads;
@@ -980,10 +999,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r >= 0 && g == 0) atomicMax(hmax + kHmaxStep * r, top);
       }
     };
-    if (tiny)
-      run_stream<FMT, 2, true, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit);
-    else
-      run_stream<FMT, 2, false, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit);
+    const bool ok =
+        tiny ? run_stream<FMT, 2, true, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit)
+             : run_stream<FMT, 2, false, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit);
+    if (!ok) return;  // the other CTAs wait at the next meeting until their own limit
   }
   {  // down + combine
     const Stream<FMT, 3> st(p, rt, wk, &map2, lane);
@@ -1032,8 +1051,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the weights do not wait for the other CTAs
     start_stream<FMT, 3>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
     if (w.lo < w.hi) next_scales<FMT, 3>(st, w, w.lo, scratch);
-    bool ok = grid_wait(barrier + 1, p.err, &wk.ok);
-    if (ok) {
+    if (!grid_wait(barrier + 1, p.err, &wk.ok)) {
+      drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);  // copies in flight land before the CTA leaves
+      return;
+    }
+    {
       if (blockIdx.x == 0 && tid == 0) p.sync[0] = 1u - parity;  // every CTA has read it
       const int pairs = p.T * p.k;  // <= 256
       // h to fp16: all of it into every CTA's shared memory, or, where that is
@@ -1069,20 +1091,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           run_stream<FMT, 3, false, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
       } else {
         grid_arrive(barrier + 2);
-        ok = grid_wait(barrier + 2, p.err, &wk.ok);
-        if (ok) {
-          if (w.lo < w.hi) st.load_h(h, w.cur);
-          if (wk.tiny)
-            run_stream<FMT, 3, true, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
-          else
-            run_stream<FMT, 3, false, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
+        if (!grid_wait(barrier + 2, p.err, &wk.ok)) {
+          drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);
+          return;
         }
-      }
-    }
-    if (!ok || wk.abort) {  // copies still in flight land before the CTA leaves
-      for (int i = 0; i < ring.stages; ++i) {
-        mbar_drain(ring.full + ring.get, ring.parity);
-        ring.popped();
+        if (w.lo < w.hi) st.load_h(h, w.cur);
+        if (wk.tiny)
+          run_stream<FMT, 3, true, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
+        else
+          run_stream<FMT, 3, false, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
       }
     }
   }
