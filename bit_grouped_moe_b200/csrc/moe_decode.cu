@@ -34,9 +34,9 @@
 //
 // MMA mapping (m16n8k16, fp16 operands, fp32 sums): A = weight codes, B =
 // activations.  A lane's codes of one scale block feed two (MXFP4) or four
-// (NF4) MMAs whose result is multiplied by the scale in fp32, so scales are not
-// rounded and not multiplied into the weights one by one.  e2m1 is exact in
-// fp16, NF4 codes are within 2^-12.  Activations are scaled by the power of two
+// (NF4) MMAs whose result is multiplied in fp32 by the activations' unit and the
+// scale, so scales are neither rounded nor multiplied into the weights one by
+// one, and sums have the range of fp32.  e2m1 is exact in fp16, NF4 codes are within 2^-12.  Activations are scaled by the power of two
 // that puts the largest of a token's x (of a (token, expert) pair's h) in
 // [2^14, 2^15): 8-bit significands of x stay exact down to 2^-28 of it, h is
 // rounded to 11 bits.  The largest of h is known when phase 2 ends (an integer
@@ -90,18 +90,12 @@ struct Work {
   uint32_t xmax[kMaxT];         // largest finite |x| of a token (fp32 bits)
   float hscale[kMaxPairs];      // scale of a pair's fp16 h
   int nhit;
-  int tiny;                     // a pair's h lies below 2^kTinyExp throughout
   int ok;
   int abort;
 };
-// Sums in units of scaled activations overflow before the true sum does; below this exponent of the largest
-// activation (a true sum of 2^50 could) blocks are brought back to true units before they are added.
-constexpr int kTinyExp = -64;
-// fp32 bits of the largest |v| -> the scale 2^(14 - e), its inverse, and whether e < kTinyExp; e at least 15 - 127.
-__device__ __forceinline__ uint32_t exp_field(uint32_t top) { return max(top >> 23, 15u); }
-__device__ __forceinline__ float scale_up(uint32_t top) { return __uint_as_float((268u - exp_field(top)) << 23); }
-__device__ __forceinline__ float scale_down(uint32_t top) { return __uint_as_float((exp_field(top) - 14u) << 23); }
-__device__ __forceinline__ bool is_tiny(uint32_t top) { return top != 0u && top < (uint32_t)(127 + kTinyExp) << 23; }
+// fp32 bits of the largest |v| -> the scale 2^(14 - e), e at least 15 - 127; and the inverse of a power of two.
+__device__ __forceinline__ float scale_up(uint32_t top) { return __uint_as_float((268u - max(top >> 23, 15u)) << 23); }
+__device__ __forceinline__ float inverse_of(float pow2) { return __uint_as_float(0x7F000000u - __float_as_uint(pow2)); }
 
 // Offsets in the dynamic shared window.  x in fragment order (in phase 3: h,
 // where there is room), Route, Work and MXFP4's scale scratch first; NF4's pair table at a 64 KB boundary (0x10000, or
@@ -476,18 +470,26 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) {
   return v;
 }
 
-// acc += scale of the row * d; TINY: d back in true units (of its column) first.
-template <bool TINY>
+// acc += scale of the row * d, d brought back to true units (of its column) first: a sum in units of the scaled
+// activations overflows 2^(14 - e) times before the true sum does.  Two values per instruction: 48 experts of 7168 /
+// 2048, T = 8, MXFP4: 187 us, one by one 190, without the step 183.
 __device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&d)[4], float sa, float sb,
                                            const float (&unit)[2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = fmaf(i < 2 ? sa : sb, TINY ? d[i] * unit[i & 1] : d[i], acc[i]);
+  for (int i = 0; i < 4; i += 2) {
+    const float sc = i < 2 ? sa : sb;
+    asm("{\n\t.reg .b64 d, u, a, s;\n\t"
+        "mov.b64 d, {%2, %3};\n\tmov.b64 u, {%4, %5};\n\tmov.b64 s, {%6, %6};\n\tmov.b64 a, {%0, %1};\n\t"
+        "mul.rn.f32x2 d, d, u;\n\tfma.rn.f32x2 a, d, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}\n"
+        : "+f"(acc[i]), "+f"(acc[i + 1])
+        : "f"(d[i]), "f"(d[i + 1]), "f"(unit[0]), "f"(unit[1]), "f"(sc));
+  }
 }
 
 // acc[tile] += the item's weights (shared memory) times the lane's activations: chunk c at x + c * x_step in shared
 // memory (HERE), else own[c].
 // Tile k holds item rows r0 + 8 STEP_T k (its first 8) and 8 STEP_H further.
-template <int FMT, bool TINY, bool HERE, int STEP_T, int STEP_H>
+template <int FMT, bool HERE, int STEP_T, int STEP_H>
 __device__ __forceinline__ void multiply(float (&acc)[2][4], uint32_t item, uint32_t scratch, uint32_t x,
                                          uint32_t x_step, const uint4 (&own)[4], const float (&unit)[2], int r0, int t,
                                          uint32_t lanesel) {
@@ -513,7 +515,7 @@ __device__ __forceinline__ void multiply(float (&acc)[2][4], uint32_t item, uint
         float d[4];
         mma_new(d, lo[0], hi[0], lo[1], hi[1], v[b].x, v[b].y);
         mma_add(d, lo[2], hi[2], lo[3], hi[3], v[b].z, v[b].w);
-        add_scaled<TINY>(acc[tile], d, sa[b], sb[b], unit);
+        add_scaled(acc[tile], d, sa[b], sb[b], unit);
       }
     }
   } else {
@@ -537,7 +539,7 @@ __device__ __forceinline__ void multiply(float (&acc)[2][4], uint32_t item, uint
                 lookup(vb.y, lanesel, 1), v1.x, v1.y);
         mma_add(d, lookup(va.y, lanesel, 2), lookup(vb.y, lanesel, 2), lookup(va.y, lanesel, 3),
                 lookup(vb.y, lanesel, 3), v1.z, v1.w);
-        add_scaled<TINY>(acc[tile], d, sa, sb, unit);
+        add_scaled(acc[tile], d, sa, sb, unit);
       }
     }
   }
@@ -630,9 +632,9 @@ struct Stream {
   // 1 / the scale of column q (0, 1) of this lane; 0 for a phase 3 column whose token did not choose expert ei.
   __device__ __forceinline__ float unit_of(int ei, int q) const {
     const int col = 2 * t + q;
-    if (PHASE == 2) return scale_down(wk.xmax[col]);
+    if (PHASE == 2) return inverse_of(scale_up(wk.xmax[col]));
     const int r = s.row[ei][col];
-    return r < 0 ? 0.f : 1.0f / wk.hscale[r];  // a power of two: exact
+    return r < 0 ? 0.f : inverse_of(wk.hscale[r]);
   }
 };
 
@@ -737,7 +739,7 @@ __device__ __forceinline__ void next_scales(const Stream<FMT, PHASE>& st, Walk<F
 // wk.abort, which ends every warp's items at its next wait: a slot whose box
 // may be in flight is neither read nor issued again.  Returns false then, in
 // all threads, with no box of the CTA in flight.
-template <int FMT, int PHASE, bool TINY, bool HERE, class Emit>
+template <int FMT, int PHASE, bool HERE, class Emit>
 __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, Work& wk,
                                            unsigned* err, uint32_t scratch, uint32_t x, uint32_t x_step,
                                            uint32_t lanesel, uint8_t* rings, int warp, uint4 (&h)[4], Emit emit) {
@@ -751,11 +753,11 @@ __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& r
   float acc[2][4] = {};
   float one[2][4] = {};   // phase 3: the current expert's part
   float head[2][4] = {};  // a unit begun by an earlier warp
-  float unit2[2] = {1.0f, 1.0f};
-  if (PHASE == 2) unit2[0] = st.unit_of(0, 0), unit2[1] = st.unit_of(0, 1);
+  float unit2[2] = {0.f, 0.f};  // of the lane's two columns; phase 3: for the current expert
+  if (lo < hi) unit2[0] = st.unit_of(w.cur.ei, 0), unit2[1] = st.unit_of(w.cur.ei, 1);
   bool tail = false;  // a unit begun by this warp and not finished by it
   for (int item = lo; item < hi; ++item) {
-    const int unit = w.cur.unit, ei = w.cur.ei, d = w.cur.d;
+    const int unit = w.cur.unit, d = w.cur.d;
     if ((d & 3) == 0 && item > lo) next_scales<FMT, PHASE>(st, w, item, scratch);
     const bool turn = st.advance(w.cur), more = item + 1 < hi;
     if (!HERE) {
@@ -763,14 +765,13 @@ __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& r
       for (int i = 0; i < 4; ++i) own[i] = h[i];
       if (more) st.load_h(h, w.cur);
     }
-    if (PHASE == 3 && TINY) unit2[0] = st.unit_of(ei, 0), unit2[1] = st.unit_of(ei, 1);
     if (!__all_sync(0xffffffffu, mbar_try_wait(ring.full + ring.get, ring.parity)) &&
         !box_wait_slow(ring.full + ring.get, ring.parity, err, &wk.abort)) {
       drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - item);
       break;
     }
     __syncwarp();
-    multiply<FMT, TINY, HERE, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(
+    multiply<FMT, HERE, PHASE == 2 ? 1 : 2, PHASE == 2 ? 2 : 1>(
         PHASE == 3 ? one : acc, ring.base + ring.get * kItemBytes, scratch + (d & 3) * kScratchItem,
         column + 4 * x_step * d, x_step, own, unit2, r0, st.t, lanesel);
     ring.popped();
@@ -782,20 +783,21 @@ __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& r
       // added as zeros: 0 times a NaN or infinite weight is NaN
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float u = st.unit_of(ei, q);
+        const bool chosen = unit2[q] != 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          acc[k][q] += u != 0.f ? (TINY ? one[k][q] : one[k][q] * u) : 0.f;
-          acc[k][q + 2] += u != 0.f ? (TINY ? one[k][q + 2] : one[k][q + 2] * u) : 0.f;
+          acc[k][q] += chosen ? one[k][q] : 0.f;
+          acc[k][q + 2] += chosen ? one[k][q + 2] : 0.f;
           one[k][q] = one[k][q + 2] = 0.f;
         }
+        if (more) unit2[q] = st.unit_of(w.cur.ei, q);
       }
       if (HERE) column = x + 256u * (uint32_t)(st.pair(w.cur.ei) * st.nd);
     }
     if (more && w.cur.unit == unit) continue;
     const int first = max(unit * per, a), last = min((unit + 1) * per, b);  // the unit's items in this CTA
     if (lo <= first && last <= hi) {
-      emit(unit, acc, last - first == per, r0, unit2);
+      emit(unit, acc, last - first == per, r0);
     } else if (lo <= first) {
       tail = true;  // stays in acc: this was the last item
       break;
@@ -834,7 +836,7 @@ __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& r
         }
       }
     }
-    emit(unit, acc, last - first == per, r0, unit2);
+    emit(unit, acc, last - first == per, r0);
   }
   return true;
 }
@@ -912,7 +914,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < kMaxT) wk.xmax[tid] = 0u;
   if (tid == 0) {
     wk.abort = 0;
-    wk.tiny = 0;
     prefetch_tmap(&map1);
     prefetch_tmap(&map2);
   }
@@ -973,23 +974,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < p.T) weigh_topk(p, rt, warp, lane, logit);  // while the first weights arrive
     if (w.lo < w.hi) next_scales<FMT, 2>(st, w, w.lo, scratch);
     __syncthreads();
-    bool tiny = false;
-    for (int i = 0; i < p.T; ++i) tiny |= is_tiny(wk.xmax[i]);
     // columns past T repeat the last token and are never stored
     const uint32_t x = kWindow + 16u * (4 * min(g, p.T - 1) + t), x_step = 64u * p.T;
-    auto emit = [&](int unit, const float(&acc)[2][4], bool, int r0, const float(&xu)[2]) {
+    auto emit = [&](int unit, const float(&acc)[2][4], bool, int r0) {
       const int ei = unit / st.cols;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tok = 2 * t + i, r = rt.row[ei][tok];
-        const float u = tiny ? 1.0f : xu[i], w = r < 0 ? 0.f : rt.sel_p[r];
+        const float w = r < 0 ? 0.f : rt.sel_p[r];
         uint32_t top = 0u;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int col = 16 * (unit - ei * st.cols) + 8 * k;  // 8 columns = one chunk
           const size_t chunk = (size_t)(col / kDK) * 16 + chunk_of<FMT>(col % kDK);
           if (r < 0) continue;
-          const float v = silu_mul(acc[k][i] * u, acc[k][2 + i] * u) * w;
+          const float v = silu_mul(acc[k][i], acc[k][2 + i]) * w;
           p.hbuf[((size_t)r * nd2 * 16 + chunk) * 8 + r0] = v;
           const uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
           top = max(top, m >= 0x7F800000u ? 0u : m);
@@ -999,10 +998,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r >= 0 && g == 0) atomicMax(hmax + kHmaxStep * r, top);
       }
     };
-    const bool ok =
-        tiny ? run_stream<FMT, 2, true, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit)
-             : run_stream<FMT, 2, false, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit);
-    if (!ok) return;  // the other CTAs wait at the next meeting until their own limit
+    if (!run_stream<FMT, 2, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit))
+      return;  // the other CTAs wait at the next meeting until their own limit
   }
   {  // down + combine
     const Stream<FMT, 3> st(p, rt, wk, &map2, lane);
@@ -1016,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tok < p.T) p.out[(size_t)tok * p.H + 32 * unit + 16 * k + r0 + 8 * (i >> 1)] = __float2bfloat16_rn(acc[k][i]);
         }
     };
-    auto emit = [&](int unit, const float(&acc)[2][4], bool whole, int r0, const float(&)[2]) {
+    auto emit = [&](int unit, const float(&acc)[2][4], bool whole, int r0) {
       if (whole) {
         store(unit, acc, r0);
         return;
@@ -1067,9 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;  // the first chunk comes along with the maxima
       if (c0 < chunks) u = __ldcg(src + 2 * c0), v = __ldcg(src + 2 * c0 + 1);
       if (tid < pairs) {
-        const uint32_t top = __ldcg(hmax + kHmaxStep * tid);
-        wk.hscale[tid] = scale_up(top);
-        if (is_tiny(top)) wk.tiny = 1;
+        wk.hscale[tid] = scale_up(__ldcg(hmax + kHmaxStep * tid));
       }
       __syncthreads();
 #pragma unroll 1
@@ -1085,10 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (here) {
         __syncthreads();
         const uint32_t x = kWindow + 16u * (uint32_t)t;
-        if (wk.tiny)
-          run_stream<FMT, 3, true, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
-        else
-          run_stream<FMT, 3, false, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
+        run_stream<FMT, 3, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
       } else {
         grid_arrive(barrier + 2);
         if (!grid_wait(barrier + 2, p.err, &wk.ok)) {
@@ -1096,10 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return;
         }
         if (w.lo < w.hi) st.load_h(h, w.cur);
-        if (wk.tiny)
-          run_stream<FMT, 3, true, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
-        else
-          run_stream<FMT, 3, false, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
+        run_stream<FMT, 3, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
       }
     }
   }

@@ -514,7 +514,9 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
  *     h[t, j]  = silu(G_e x[t]) * (U_e x[t]),  e = topk_ids[t, j], G_e / U_e
  *       rows [0, I) / [I, 2I) of w_gate_up[e],
  *     out[t]   = sum_j topk_weights[t, j] * (D_e h[t, j]),  D_e = w_down[e].
- * Sums and scales are fp32, out is rounded once to bf16.  The products run on
+ * Sums and scales are fp32 and have its range; where e^-g overflows towards it
+ * (a gate value below -87.3) silu counts as 0; out is rounded once to bf16.
+ * The products run on
  * fp16 values that a power of two brings into range: x (scaled by the token's
  * largest; its bf16 values are exact down to 2^-28 of that, and within 2^-39
  * of it below), topk_weights[t, j] * h[t, j] (scaled by the
