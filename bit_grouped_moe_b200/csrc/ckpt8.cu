@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(row_threads(WPR), 1280 / row_threads(WPR)) swi
         hv[i] = gsig * u[i];
         dot = fmaf(d[i], hv[i], dot);
         const float wd = w * d[i];
-        g[i] = slope * u[i] * wd;
+        g[i] = slope * (u[i] * wd);  // slope (at most 1.1) times the largest u may pass fp32
         u[i] = gsig * wd;
       }
       dgu[row + c] = pack8(g);
