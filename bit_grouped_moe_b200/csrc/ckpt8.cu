@@ -5,8 +5,9 @@
 // gate_up values as MXFP8: per 32 consecutive values X = max(floor(log2(max
 // |v|)) - 7, -127), code = e4m3(v * 2^-X), ties to even.  The exponent leaves
 // one binade of headroom (as the two-term split's hi term does), so nothing
-// saturates and every element keeps 4 significant bits down to 2^-13 of the
-// block's largest; the OCP exponent (- 8) would clip values above 448/512 of
+// saturates (but 1.9375 2^127 and above, kept as 1.875 2^127: the next e4m3
+// value is no fp32 number) and every element keeps 4 significant bits down to
+// 2^-13 of the block's largest; the OCP exponent (- 8) would clip values above 448/512 of
 // their binade by up to 1/8.  A non-finite value is stored as the e4m3 NaN
 // and does not enter its block's scale.
 //
@@ -151,8 +152,9 @@ __device__ __forceinline__ uint2 quant8(uint4 v, const F2 (&f)[4], uint32_t* sca
   m = max(m & 0xFFFFu, m >> 16);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const bool wild = m >= 0x7F80u;  // the block holds an infinity or a NaN: they stay out of its maximum
-  if (__any_sync(0xffffffffu, wild)) {
+  const bool rare = m >= 0x7F00u;  // values from 2^127 on, or an infinity or a NaN, which stay out of the maximum
+  const bool any_rare = __any_sync(0xffffffffu, rare);
+  if (any_rare) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t n = 0;
 #pragma unroll
@@ -169,13 +171,19 @@ __device__ __forceinline__ uint2 quant8(uint4 v, const F2 (&f)[4], uint32_t* sca
   uint32_t out[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 a = split(mul2(f[i], both(inv)));
-    if (wild) {  // the finite-saturating conversion would store an infinity as 448: inf - inf is NaN, 0 otherwise
-      const float2 b = split(f[i]);
-      a.x += b.x - b.x;
-      a.y += b.y - b.y;
-    }
+    const float2 a = split(mul2(f[i], both(inv)));
     out[i >> 1] |= cvt_e4m3x2(a.y, a.x) << (16 * (i & 1));
+  }
+  if (any_rare) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 p = split(f[i >> 1]);
+      const uint32_t at = 8 * (i & 3), c = (out[i >> 2] >> at) & 0x7Fu;
+      if (!isfinite(i & 1 ? p.y : p.x))  // the conversion stores an infinity as 448
+        out[i >> 2] = (out[i >> 2] & ~(0xFFu << at)) | (0x7Fu << at);
+      else if (X == 120 && c == 0x78u)  // 256 2^120 is no fp32 number: the value below, 240
+        out[i >> 2] -= 1u << at;
+    }
   }
   *scale = (uint32_t)(X + 127);
   return make_uint2(out[0], out[1]);
@@ -188,12 +196,12 @@ __device__ __forceinline__ int live_rows(const int* num_rows, int M) {
 // One thread, PER times: 8 gate values, the 8 matching up values, 8 outputs.
 // All loads of a thread are issued before the first is used.  32768 rows of
 // 2048: 86 us (6.3 TB/s) with PER = 4, 9 us more with 1; 72 rows of 1024: 2.0
-// us with 1, 3.6 with 4, so few values take 1.
+// us with 1, 3.6 with 4, so few values take 1.  64 registers (4 CTAs per SM): 8 us
+// less than the 76 the compiler takes by itself.
 template <typename Idx, int PER>
-__global__ void __launch_bounds__(kThreads) swiglu_ckpt8_kernel(const __nv_bfloat16* __restrict__ gate_up, int M,
-                                                                int I8, const int* __restrict__ num_rows,
-                                                                uint4* __restrict__ h, uint2* __restrict__ codes,
-                                                                uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(kThreads, PER == 4 && sizeof(Idx) == 4 ? 4 : 1)
+    swiglu_ckpt8_kernel(const __nv_bfloat16* __restrict__ gate_up, int M, int I8, const int* __restrict__ num_rows,
+                        uint4* __restrict__ h, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
   griddep_launch_dependents();
   griddep_wait();
   const int rows = live_rows(num_rows, M);

@@ -580,8 +580,10 @@ gnf4_status gnf4_moe_decode_mxfp4(const void *x, const void *router_w, const flo
  *     h[r, i] = silu(gate_up[r, i]) * gate_up[r, I + i]         (fp32, one rounding to bf16),
  *     codes / scales[r]: the 2I values as MXFP8 with X = max(floor(log2(max|v|)) - 7, -127)
  *       per 32 consecutive values, scale byte X + 127, code = v * 2^-X rounded to
- *       the nearest e4m3 value, ties to even: nothing saturates.  Non-finite
- *       values become the e4m3 NaN and do not enter the block's maximum.
+ *       the nearest e4m3 value, ties to even: nothing saturates, but that values
+ *       of 1.9375 * 2^127 and above are stored as 1.875 * 2^127 (they would round
+ *       to 2^128, which fp32 does not hold).  Non-finite values become the e4m3
+ *       NaN and do not enter the block's maximum.
  *   gate_up bf16 [M, 2I] (gate values first); num_rows int32 [1] on the device
  *   or NULL (= M; offsets + E of the routing is what a sorted batch passes):
  *   rows at and past it are neither read nor written; h bf16 [M, I] OUT; codes uint8
