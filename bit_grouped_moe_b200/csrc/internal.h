@@ -192,8 +192,10 @@ struct MoeDecodeArgs {
   float* logits;                  // [T, E]
   const uint8_t* w1;              // [E, 2I, H/2]
   const void* s1;
+  const void* s1_end;             // past the last scale
   const uint8_t* w2;              // [E, H, I/2]
   const void* s2;
+  const void* s2_end;
   int* topk_ids;                  // [T, k]
   float* topk_weights;            // [T, k]
   __nv_bfloat16* out;             // [T, H]

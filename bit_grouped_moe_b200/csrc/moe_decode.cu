@@ -399,17 +399,34 @@ struct ScaleGroup {
   uint32_t off;  // the first scale's byte in q
 };
 
-// row: the row's first scale; bytes: of the row; group: 512-k group.  Blocks without a byte of the group are not read.
-template <int FMT>
-__device__ __forceinline__ void load_scales(ScaleGroup<FMT>& s, const uint8_t* row, int bytes, int group) {
-  constexpr int kBytes = FMT == 0 ? 32 : 16;
+// The 16-byte block at b, whose bytes outside [lo, hi) are not read: 0.
+__device__ __noinline__ uint4 load_edge(uintptr_t b, uintptr_t lo, uintptr_t hi) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  for (int i = 0; i < 16; ++i)
+    if (b + i >= lo && b + i < hi) w[i >> 2] |= (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(b + i)) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// row: the row's first scale; bytes: of the row; group: 512-k group; [lo, hi): the array.  Blocks without a byte of
+// the group are not read.  EDGES: an array that begins at no 16-byte boundary shares its first and its last block
+// with other memory; blocks that stick out are read byte by byte.
+template <int FMT, bool EDGES>
+__device__ __forceinline__ void load_scales(ScaleGroup<FMT>& s, const uint8_t* row, int bytes, int group,
+                                            const void* lo, const void* hi) {
+  constexpr int kBytes = FMT == 0 ? 32 : 16, kBlocks = FMT == 0 ? 3 : 2;
   const uintptr_t a = reinterpret_cast<uintptr_t>(row) + (size_t)group * kBytes;
-  const uintptr_t down = a & ~(uintptr_t)15;
+  const uintptr_t down = a & ~(uintptr_t)15, first = reinterpret_cast<uintptr_t>(lo), end = reinterpret_cast<uintptr_t>(hi);
   s.off = (uint32_t)(a & 15);
   const int need = (int)s.off + min(bytes - group * kBytes, kBytes);
+  if (!EDGES || (down >= first && down + ((need + 15) & ~15) <= end)) {
 #pragma unroll
-  for (int i = 0; i < (FMT == 0 ? 3 : 2); ++i)
-    s.q[i] = 16 * i < need ? ldg_u128(reinterpret_cast<const void*>(down + 16 * i)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kBlocks; ++i)
+      s.q[i] = 16 * i < need ? ldg_u128(reinterpret_cast<const void*>(down + 16 * i)) : make_uint4(0u, 0u, 0u, 0u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+      s.q[i] = 16 * i < need ? load_edge(down + 16 * i, first, end) : make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 
 // The group as fp32 in the warp's scratch (this lane's row).  left: scales from the group on (a scale past K is
@@ -610,13 +627,15 @@ struct Stream {
     else
       tma_load_3d(dst, map, bar, (kDK / 2) * c.d, 32 * c.unit, e);
   }
+  __device__ __forceinline__ const void* scales() const { return PHASE == 2 ? p.s1 : p.s2; }
+  __device__ __forceinline__ const void* scales_end() const { return PHASE == 2 ? p.s1_end : p.s2_end; }
   // First scale of item row `lane`.
   __device__ __forceinline__ const uint8_t* scale_row(const Cursor& c) const {
     const size_t e = (size_t)s.expert[c.ei];
     const size_t n = PHASE == 2 ? e * (2 * (size_t)p.I) + 16 * (size_t)(c.unit - c.ei * cols) + (lane & 15) +
                                       (lane < 16 ? 0 : (size_t)p.I)
                                 : e * (size_t)p.H + 32 * (size_t)c.unit + lane;
-    return static_cast<const uint8_t*>(PHASE == 2 ? p.s1 : p.s2) + n * (size_t)srow;
+    return static_cast<const uint8_t*>(scales()) + n * (size_t)srow;
   }
   // Phase 3: the pair whose h this lane multiplies (a column without the token takes another: its sums are dropped).
   __device__ __forceinline__ int pair(int ei) const {
@@ -693,7 +712,7 @@ __device__ __forceinline__ void issue_box(const Stream<FMT, PHASE>& st, Ring& ri
 }
 
 // The first boxes and scales on their way.
-template <int FMT, int PHASE>
+template <int FMT, int PHASE, bool EDGES>
 __device__ __forceinline__ void start_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, int a, int b,
                                              int warp) {
   const int n = b - a;
@@ -708,25 +727,25 @@ __device__ __forceinline__ void start_stream(const Stream<FMT, PHASE>& st, Ring&
   for (int i = 0; i < ring.stages; ++i) issue_box(st, ring, w);
   if (w.lo < w.hi) {
     w.row = st.scale_row(w.cur);
-    load_scales<FMT>(w.sc, w.row, st.srow, w.cur.d >> 2);
+    load_scales<FMT, EDGES>(w.sc, w.row, st.srow, w.cur.d >> 2, st.scales(), st.scales_end());
   }
 }
 
 // The loaded scale group (the one of item `item` at cur) to the scratch, and the one after it on its way.
-template <int FMT, int PHASE>
+template <int FMT, int PHASE, bool EDGES>
 __device__ __forceinline__ void next_scales(const Stream<FMT, PHASE>& st, Walk<FMT>& w, int item, uint32_t scratch) {
   const int group = w.cur.d >> 2;
   scales_to_scratch<FMT>(w.sc, st.ns - group * (FMT == 0 ? 8 : 16), scratch, st.lane);
   const int skip = min(4 - (w.cur.d & 3), st.nd - w.cur.d);
   if (item + skip >= w.hi) return;  // no other group belongs to this warp
   if (w.cur.d + skip < st.nd) {
-    load_scales<FMT>(w.sc, w.row, st.srow, group + 1);
+    load_scales<FMT, EDGES>(w.sc, w.row, st.srow, group + 1, st.scales(), st.scales_end());
   } else {
     Cursor q = w.cur;
     q.d = st.nd - 1;
     st.advance(q);
     w.row = st.scale_row(q);
-    load_scales<FMT>(w.sc, w.row, st.srow, 0);
+    load_scales<FMT, EDGES>(w.sc, w.row, st.srow, 0, st.scales(), st.scales_end());
   }
 }
 
@@ -739,7 +758,7 @@ __device__ __forceinline__ void next_scales(const Stream<FMT, PHASE>& st, Walk<F
 // wk.abort, which ends every warp's items at its next wait: a slot whose box
 // may be in flight is neither read nor issued again.  Returns false then, in
 // all threads, with no box of the CTA in flight.
-template <int FMT, int PHASE, bool HERE, class Emit>
+template <int FMT, int PHASE, bool EDGES, bool HERE, class Emit>
 __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& ring, Walk<FMT>& w, Work& wk,
                                            unsigned* err, uint32_t scratch, uint32_t x, uint32_t x_step,
                                            uint32_t lanesel, uint8_t* rings, int warp, uint4 (&h)[4], Emit emit) {
@@ -758,7 +777,7 @@ __device__ __forceinline__ bool run_stream(const Stream<FMT, PHASE>& st, Ring& r
   bool tail = false;  // a unit begun by this warp and not finished by it
   for (int item = lo; item < hi; ++item) {
     const int unit = w.cur.unit, d = w.cur.d;
-    if ((d & 3) == 0 && item > lo) next_scales<FMT, PHASE>(st, w, item, scratch);
+    if ((d & 3) == 0 && item > lo) next_scales<FMT, PHASE, EDGES>(st, w, item, scratch);
     const bool turn = st.advance(w.cur), more = item + 1 < hi;
     if (!HERE) {
 #pragma unroll
@@ -886,7 +905,7 @@ __device__ __forceinline__ void stage_x(const MoeDecodeArgs& p, Work& s, uint4* 
   }
 }
 
-template <int FMT>
+template <int FMT, bool EDGES>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_decode_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
                       const MoeDecodeArgs p, const Plan plan) {
@@ -970,9 +989,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   {  // gate_up + SwiGLU; h times its router weight goes to the workspace in fragment order
     const Stream<FMT, 2> st(p, rt, wk, &map1, lane);
     const Share sh(wk.nhit * st.cols, gridDim.x);
-    start_stream<FMT, 2>(st, ring, w, sh.begin(blockIdx.x) * st.per, sh.begin(blockIdx.x + 1) * st.per, warp);
+    start_stream<FMT, 2, EDGES>(st, ring, w, sh.begin(blockIdx.x) * st.per, sh.begin(blockIdx.x + 1) * st.per, warp);
     if (warp < p.T) weigh_topk(p, rt, warp, lane, logit);  // while the first weights arrive
-    if (w.lo < w.hi) next_scales<FMT, 2>(st, w, w.lo, scratch);
+    if (w.lo < w.hi) next_scales<FMT, 2, EDGES>(st, w, w.lo, scratch);
     __syncthreads();
     // columns past T repeat the last token and are never stored
     const uint32_t x = kWindow + 16u * (4 * min(g, p.T - 1) + t), x_step = 64u * p.T;
@@ -998,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r >= 0 && g == 0) atomicMax(hmax + kHmaxStep * r, top);
       }
     };
-    if (!run_stream<FMT, 2, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit))
+    if (!run_stream<FMT, 2, EDGES, true>(st, ring, w, wk, p.err, scratch, x, x_step, lanesel, rings, warp, h, emit))
       return;  // the other CTAs wait at the next meeting until their own limit
   }
   {  // down + combine
@@ -1046,8 +1065,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     grid_arrive(barrier + 1);
     // the weights do not wait for the other CTAs
-    start_stream<FMT, 3>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
-    if (w.lo < w.hi) next_scales<FMT, 3>(st, w, w.lo, scratch);
+    start_stream<FMT, 3, EDGES>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
+    if (w.lo < w.hi) next_scales<FMT, 3, EDGES>(st, w, w.lo, scratch);
     if (!grid_wait(barrier + 1, p.err, &wk.ok)) {
       drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);  // copies in flight land before the CTA leaves
       return;
@@ -1080,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (here) {
         __syncthreads();
         const uint32_t x = kWindow + 16u * (uint32_t)t;
-        run_stream<FMT, 3, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
+        run_stream<FMT, 3, EDGES, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
       } else {
         grid_arrive(barrier + 2);
         if (!grid_wait(barrier + 2, p.err, &wk.ok)) {
@@ -1088,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return;
         }
         if (w.lo < w.hi) st.load_h(h, w.cur);
-        run_stream<FMT, 3, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
+        run_stream<FMT, 3, EDGES, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
       }
     }
   }
@@ -1144,14 +1163,14 @@ size_t moe_decode_workspace(int T, int k, int I, size_t* at) {
   return align256(n + (size_t)T * k * ((I + kDK - 1) / kDK) * kDK * 2);
 }
 
-template <int FMT>
+template <int FMT, bool EDGES>
 static cudaError_t launch_t(const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p, int num_sms,
                             cudaStream_t stream) {
   static std::atomic<bool> configured[64];
   const Plan plan = make_plan(FMT, p.T, p.H, p.T * p.k, p.I);
   const int grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
   if (plan.stages < 1 || p.E > 8 * grid) return cudaErrorInvalidConfiguration;  // the router: 8 experts a CTA
-  cudaError_t e = set_smem_limit_once(moe_decode_kernel<FMT>, (int)kMaxWindow, configured);
+  cudaError_t e = set_smem_limit_once(moe_decode_kernel<FMT, EDGES>, (int)kMaxWindow, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -1163,12 +1182,17 @@ static cudaError_t launch_t(const CUtensorMap& map1, const CUtensorMap& map2, co
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_decode_kernel<FMT>, map1, map2, p, plan);
+  return cudaLaunchKernelEx(&cfg, moe_decode_kernel<FMT, EDGES>, map1, map2, p, plan);
 }
 
 cudaError_t launch_moe_decode(int fmt, const CUtensorMap& map1, const CUtensorMap& map2, const MoeDecodeArgs& p,
                               int num_sms, cudaStream_t stream) {
-  return fmt == 0 ? launch_t<0>(map1, map2, p, num_sms, stream) : launch_t<1>(map1, map2, p, num_sms, stream);
+  // Scale arrays that begin at 16-byte boundaries (as allocations do) need no look at their ends, which costs 2 to 5%:
+  // NF4, OLMoE shape, T = 8 61.1 us instead of 59.1, MXFP4, 64 experts of 2048 / 1024, T = 4 41.9 instead of 39.4.
+  const bool edges = ((reinterpret_cast<uintptr_t>(p.s1) | reinterpret_cast<uintptr_t>(p.s2)) & 15) != 0;
+  if (fmt == 0)
+    return edges ? launch_t<0, true>(map1, map2, p, num_sms, stream) : launch_t<0, false>(map1, map2, p, num_sms, stream);
+  return edges ? launch_t<1, true>(map1, map2, p, num_sms, stream) : launch_t<1, false>(map1, map2, p, num_sms, stream);
 }
 
 }  // namespace gnf4
