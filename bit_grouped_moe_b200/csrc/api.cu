@@ -1109,8 +1109,7 @@ static gnf4_status moe_decode_impl(int fmt, const void* x, const void* router_w,
   p.router_w = static_cast<const __nv_bfloat16*>(router_w);
   p.bias = bias;
   p.logits = logits;
-  p.w1 = w_gate_up, p.s1 = scales_gate_up;
-  p.w2 = w_down, p.s2 = scales_down;
+  p.s1 = scales_gate_up, p.s2 = scales_down;
   const size_t sbytes = fmt == 0 ? 4 : 1;  // of a scale, one per kq values: both arrays' sizes are multiples of 16
   p.s1_end = static_cast<const uint8_t*>(p.s1) + (size_t)E * 2 * I * (H / kq) * sbytes;
   p.s2_end = static_cast<const uint8_t*>(p.s2) + (size_t)E * H * (I / kq) * sbytes;

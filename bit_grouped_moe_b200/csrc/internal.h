@@ -190,11 +190,9 @@ struct MoeDecodeArgs {
   const __nv_bfloat16* router_w;  // [E, H] or null: logits are given
   const float* bias;              // [E] or null
   float* logits;                  // [T, E]
-  const uint8_t* w1;              // [E, 2I, H/2]
-  const void* s1;
+  const void* s1;                 // scales of gate_up [E, 2I, H / 64 or 32]; the codes come through the tensor maps
   const void* s1_end;             // past the last scale
-  const uint8_t* w2;              // [E, H, I/2]
-  const void* s2;
+  const void* s2;                 // of down [E, H, I / 64 or 32]
   const void* s2_end;
   int* topk_ids;                  // [T, k]
   float* topk_weights;            // [T, k]
