@@ -52,11 +52,13 @@
 // the per-lane pair table of the grouped GEMV (one PRMT and one shared load).
 // Rounded to 16 bits apart from that: out, once.
 //
-// Bound: 18 to 23 us of a call are latency (three meetings of the grid, two
-// pipeline starts, the cross-CTA tail).  In the loops MXFP4 is bound by HBM
-// (5.6-5.9 TB/s; the loads alone 6.6), NF4 by shared memory (122 cycles per
-// item, of which 64 are lookups: 5.3 TB/s; measured 4.2).  Calls: OLMoE shape
-// T = 1 26 us, T = 8 68 us; 7168 / 2048, 48 experts, T = 8, MXFP4 184 us.
+// Bound: 16 to 23 us of a call are latency: the meetings of the grid (one behind
+// the router product, one behind phase 2, one more where h is too large for
+// shared memory), two pipeline starts, the cross-CTA tail.  In the loops MXFP4
+// is bound by HBM (5.0-5.4 TB/s; the loads alone 6.6), NF4 by shared memory (122
+// cycles per item, of which 64 are lookups: 5.3 TB/s; measured 4.4-5).  Calls:
+// OLMoE shape T = 1 25 us, T = 8 60 us; 7168 / 2048, 48 experts, T = 8, MXFP4
+// 182 to 190 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1120,9 +1122,9 @@ Plan make_plan(int fmt, int T, int H, int pairs, int I) {
   auto up = [](uint32_t n, uint32_t a) { return (n + a - 1) / a * a; };
   const uint32_t x = (uint32_t)((H + kDK - 1) / kDK) * 256u * (uint32_t)T;
   // Room for all of h where that is cheaper than sharing the conversion and meeting once more.  MXFP4: 23 KB (T = 1,
-  // k = 4, I = 2880) 32.5 us instead of 34.5, 64 KB (T = 4, k = 8, I = 1024) 39.9 instead of 40.6, but 128 KB 56.9
-  // instead of 53.0.  NF4: 32 KB 33.8 instead of 34.5, but 64 KB, which moves the table, 48.2 instead of 47.4.  An x
-  // that is larger leaves the room anyway.
+  // k = 4, I = 2880) 31.6 us instead of 33.5, 64 KB (T = 4, k = 8, I = 1024) 39.0 instead of 40.6, but 128 KB (T = 8)
+  // 55.4 instead of 53.6.  NF4: 32 KB (T = 4, k = 8, I = 512) 30.0 instead of 30.7, but 64 KB (I = 1024), which moves
+  // the table, 44.7 instead of 44.2.  An x that is larger leaves the room anyway.
   const uint32_t h = (uint32_t)pairs * (uint32_t)((I + kDK - 1) / kDK) * 256u;
   const uint32_t limit = fmt == 0 ? 32768u : 65536u;
   q.act = x;

@@ -514,12 +514,10 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
  *     h[t, j]  = silu(G_e x[t]) * (U_e x[t]),  e = topk_ids[t, j], G_e / U_e
  *       rows [0, I) / [I, 2I) of w_gate_up[e],
  *     out[t]   = sum_j topk_weights[t, j] * (D_e h[t, j]),  D_e = w_down[e].
- * Sums and scales are fp32 and have its range; where e^-g overflows towards it
- * (a gate value below -87.3) silu counts as 0; out is rounded once to bf16.
- * The products run on
- * fp16 values that a power of two brings into range: x (scaled by the token's
- * largest; its bf16 values are exact down to 2^-28 of that, and within 2^-39
- * of it below), topk_weights[t, j] * h[t, j] (scaled by the pair's largest;
+ * Sums and scales are fp32 and have its range; silu of a gate value below -87.3
+ * counts as 0; out is rounded once to bf16.  The products run on fp16 values
+ * that a power of two brings into range: x (scaled by the token's largest; its
+ * bf16 values are exact down to 2^-28 of that, and within 2^-39 of it below), topk_weights[t, j] * h[t, j] (scaled by the pair's largest;
  * rounded to 11 bits down to 2^-28 of that, and within 2^-39 of it below), the
  * NF4 codes (within 2^-12) and the MXFP4 codes (exact).  Two calls with the
  * same inputs give the same bits.
@@ -573,6 +571,7 @@ gnf4_status gnf4_moe_decode_mxfp4(const void *x, const void *router_w, const flo
  *               dx_sorted = gnf4_grouped_dgrad_*(d_gate_up, w_gate_up);
  *               dx = gnf4_combine(dx_sorted, weights all 1);
  *               gnf4_route_topk_backward(d_weights) -> d_logits.
+ * Every pointer must be memory of the current device (or managed).
  * Between the passes only the codes, the scales and the routing are kept:
  * neither gate_up, h nor y.  (The pages name the dgrad and the checkpointed
  * layer but no 8-bit form: this is a reading.)
