@@ -23,7 +23,8 @@ constexpr int kWarps = kThreads / 32;
 // WPR warps per row; one lane moves 8 values with 16-byte loads and stores.
 // Rows in their own order: y and dy stream, and a token's dout is read k times
 // from the L2.  2048 tokens, top-8, 2048 wide: 28.6 us (a plain copy of the
-// same bytes 25), as a gather 14.9 (floor 11.7), 4096 tokens 27.0 (23.4); in the order of the pairs, whose warps share dout in the L1
+// same bytes 25), as a gather 14.9 (floor 11.7; 4096 tokens 27.0, floor 23.4);
+// in the order of the pairs, whose warps share dout in the L1
 // but scatter the rows, 30.0; with four pieces of a row unrolled 33.3.
 template <int WPR>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(

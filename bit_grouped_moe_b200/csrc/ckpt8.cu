@@ -7,8 +7,8 @@
 // one binade of headroom (as the two-term split's hi term does), so nothing
 // saturates (but 1.9375 2^127 and above, kept as 1.875 2^127: the next e4m3
 // value is no fp32 number) and every element keeps 4 significant bits down to
-// 2^-13 of the block's largest; the OCP exponent (- 8) would clip values above 448/512 of
-// their binade by up to 1/8.  A non-finite value is stored as the e4m3 NaN
+// 2^-13 of the block's largest; the OCP exponent (- 8) would clip values above
+// 448/512 of their binade by up to 1/8.  A non-finite value is stored as the e4m3 NaN
 // and does not enter its block's scale.
 //
 // Backward, per row with router weight w (1 without routing), from the

@@ -36,7 +36,8 @@
 // activations.  A lane's codes of one scale block feed two (MXFP4) or four
 // (NF4) MMAs whose result is multiplied in fp32 by the activations' unit and the
 // scale, so scales are neither rounded nor multiplied into the weights one by
-// one, and sums have the range of fp32.  e2m1 is exact in fp16, NF4 codes are within 2^-12.  Activations are scaled by the power of two
+// one, and sums have the range of fp32.  e2m1 is exact in fp16, NF4 codes are
+// within 2^-12.  Activations are scaled by the power of two
 // that puts the largest of a token's x (of a (token, expert) pair's h) in
 // [2^14, 2^15): 8-bit significands of x stay exact down to 2^-28 of it, h is
 // rounded to 11 bits.  The largest of h is known when phase 2 ends (an integer
@@ -1070,47 +1071,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     start_stream<FMT, 3, EDGES>(st, ring, w, sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), warp);
     if (w.lo < w.hi) next_scales<FMT, 3, EDGES>(st, w, w.lo, scratch);
     if (!grid_wait(barrier + 1, p.err, &wk.ok)) {
-      drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);  // copies in flight land before the CTA leaves
+      // copies in flight land before the CTA leaves
+      drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);
       return;
     }
-    {
-      if (blockIdx.x == 0 && tid == 0) p.sync[0] = 1u - parity;  // every CTA has read it
-      const int pairs = p.T * p.k;  // <= 256
-      // h to fp16: all of it into every CTA's shared memory, or, where that is
-      // too small, each CTA a share in global memory and one more barrier
-      const float4* src = reinterpret_cast<const float4*>(p.hbuf);
-      const int chunks = pairs * nd2 * 16;  // of 8 values
-      const bool here = (uint32_t)chunks * 16u <= plan.act;
-      const int c0 = here ? tid : (int)(blockIdx.x * kThreads) + tid, cs = here ? kThreads : (int)gridDim.x * kThreads;
-      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;  // the first chunk comes along with the maxima
-      if (c0 < chunks) u = __ldcg(src + 2 * c0), v = __ldcg(src + 2 * c0 + 1);
-      if (tid < pairs) {
-        wk.hscale[tid] = scale_up(__ldcg(hmax + kHmaxStep * tid));
-      }
-      __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) p.sync[0] = 1u - parity;  // every CTA has read it
+    const int pairs = p.T * p.k;  // <= 256
+    // h to fp16: all of it into every CTA's shared memory, or, where that is
+    // too small, each CTA a share in global memory and one more barrier
+    const float4* src = reinterpret_cast<const float4*>(p.hbuf);
+    const int chunks = pairs * nd2 * 16;  // of 8 values
+    const bool here = (uint32_t)chunks * 16u <= plan.act;
+    const int c0 = here ? tid : (int)(blockIdx.x * kThreads) + tid, cs = here ? kThreads : (int)gridDim.x * kThreads;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;  // the first chunk comes along with the maxima
+    if (c0 < chunks) u = __ldcg(src + 2 * c0), v = __ldcg(src + 2 * c0 + 1);
+    if (tid < pairs) wk.hscale[tid] = scale_up(__ldcg(hmax + kHmaxStep * tid));
+    __syncthreads();
 #pragma unroll 1
-      for (int i = c0; i < chunks;) {
-        const float sc = wk.hscale[i / (nd2 * 16)];
-        __half2 q[4] = {__floats2half2_rn(u.x * sc, u.y * sc), __floats2half2_rn(u.z * sc, u.w * sc),
-                        __floats2half2_rn(v.x * sc, v.y * sc), __floats2half2_rn(v.z * sc, v.w * sc)};
-        const int to = i;
-        i += cs;
-        if (i < chunks) u = __ldcg(src + 2 * i), v = __ldcg(src + 2 * i + 1);
-        *(here ? reinterpret_cast<uint4*>(smem_raw) + to : p.h16 + to) = *reinterpret_cast<uint4*>(q);
+    for (int i = c0; i < chunks;) {
+      const float sc = wk.hscale[i / (nd2 * 16)];
+      __half2 q[4] = {__floats2half2_rn(u.x * sc, u.y * sc), __floats2half2_rn(u.z * sc, u.w * sc),
+                      __floats2half2_rn(v.x * sc, v.y * sc), __floats2half2_rn(v.z * sc, v.w * sc)};
+      const int to = i;
+      i += cs;
+      if (i < chunks) u = __ldcg(src + 2 * i), v = __ldcg(src + 2 * i + 1);
+      *(here ? reinterpret_cast<uint4*>(smem_raw) + to : p.h16 + to) = *reinterpret_cast<uint4*>(q);
+    }
+    if (here) {
+      __syncthreads();
+      const uint32_t x = kWindow + 16u * (uint32_t)t;
+      run_stream<FMT, 3, EDGES, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
+    } else {
+      grid_arrive(barrier + 2);
+      if (!grid_wait(barrier + 2, p.err, &wk.ok)) {
+        drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);
+        return;
       }
-      if (here) {
-        __syncthreads();
-        const uint32_t x = kWindow + 16u * (uint32_t)t;
-        run_stream<FMT, 3, EDGES, true>(st, ring, w, wk, p.err, scratch, x, 64u, lanesel, rings, warp, h, emit);
-      } else {
-        grid_arrive(barrier + 2);
-        if (!grid_wait(barrier + 2, p.err, &wk.ok)) {
-          drain_boxes(ring.full, ring.stages, ring.get, ring.parity, w.next - w.lo);
-          return;
-        }
-        if (w.lo < w.hi) st.load_h(h, w.cur);
-        run_stream<FMT, 3, EDGES, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
-      }
+      if (w.lo < w.hi) st.load_h(h, w.cur);
+      run_stream<FMT, 3, EDGES, false>(st, ring, w, wk, p.err, scratch, 0u, 0u, lanesel, rings, warp, h, emit);
     }
   }
 }

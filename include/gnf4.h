@@ -517,10 +517,11 @@ gnf4_status gnf4_combine(const void *y, const int32_t *flat_to_sorted, const flo
  * Sums and scales are fp32 and have its range; silu of a gate value below -87.3
  * counts as 0; out is rounded once to bf16.  The products run on fp16 values
  * that a power of two brings into range: x (scaled by the token's largest; its
- * bf16 values are exact down to 2^-28 of that, and within 2^-39 of it below), topk_weights[t, j] * h[t, j] (scaled by the pair's largest;
- * rounded to 11 bits down to 2^-28 of that, and within 2^-39 of it below), the
- * NF4 codes (within 2^-12) and the MXFP4 codes (exact).  Two calls with the
- * same inputs give the same bits.
+ * bf16 values are exact down to 2^-28 of that, and within 2^-39 of it below),
+ * topk_weights[t, j] * h[t, j] (scaled by the pair's largest; rounded to 11
+ * bits down to 2^-28 of that, and within 2^-39 of it below), the NF4 codes
+ * (within 2^-12) and the MXFP4 codes (exact).  Two calls with the same inputs
+ * give the same bits.
  *   x             bf16 [T, H];
  *   router_w      bf16 [E, H], or NULL: logits are then an input;
  *   bias          fp32 [E] or NULL: added for the selection only;
